@@ -507,6 +507,120 @@ PKV_API pkv_status pkv_attention_prefill(void* out, const void* q, int32_t q_dty
 #define PKV_PREFILL_TCGEN05 2
 PKV_API pkv_status pkv_set_prefill_kernel(int32_t kind);
 
+/* ------------------------------------------------ append with rotation
+ * The write side of a serving step on the keys and queries as a projection
+ * gives them: positions rotated in, through the block table, into any cache
+ * the library has, among them an E4M3 cache with one scale per (block, KV
+ * head).  ([C "In and out"]: the step writes the new tokens' K/V into the
+ * reserved slots; the pages describe no rotation and no block scales, both
+ * are the library's.) */
+
+/* Rotary position encoding of pkv_append, on the first rotary_dim elements of
+ * each K and q row: with r = rotary_dim and the position's table row (cos
+ * a_0 .. cos a_{r/2-1}, sin a_0 .. sin a_{r/2-1}), pair i becomes
+ *   (x0 cos a_i - x1 sin a_i, x0 sin a_i + x1 cos a_i),
+ * both products and their sum rounded to fp32.  Pair i is elements (i, i +
+ * r/2), or (2i, 2i + 1) if interleaved. */
+typedef struct {
+  const float* cos_sin;  /* device float32 [max_position][rotary_dim], 16-byte aligned */
+  int32_t max_position;  /* rows of the table */
+  int32_t rotary_dim;    /* a multiple of 16, at most head_dim; 0: no rotation */
+  int32_t interleaved;
+} pkv_rope;
+
+/* Write the new tokens of a batch, K (and optionally q) rotated by their
+ * position.  The chunk of sequence s is its last n_s = query_start[s+1] -
+ * query_start[s] logical positions ctx_s - n_s .. ctx_s - 1, as in
+ * pkv_attention_prefill; the token at position p goes to slot p % T of block
+ * block_tables[s][p / T], K at angle p, V as it is.
+ *   k, v          : device, token i's [num_kv_heads][head_dim] at element
+ *                   offset i * k_stride (v_stride): views of a packed
+ *                   projection need no copy.  src_dtype as for pkv_write.
+ *   q, q_out      : q likewise (q_stride); q_out device [total_tokens]
+ *                   [num_q_heads][head_dim] of src_dtype receives it rotated
+ *                   and may be q itself if that is contiguous.  NULL with
+ *                   num_q_heads 0.
+ *                   Strides in elements, at least one row, rows on 16-byte
+ *                   boundaries.
+ *   block_scales  : NULL, or (E4M3 caches without head_scales) device float32
+ *                   [num_blocks][num_kv_heads][2], 8-byte aligned: each
+ *                   block's K and V scale of each KV head, zero-filled before
+ *                   the first use.  A touched block's scale becomes the larger
+ *                   of what it was (only where the block holds earlier tokens
+ *                   of the sequence) and the least power of two s, from 2^-40
+ *                   to 2^40, with |x| <= 448 s for the new finite x; when it
+ *                   grows, the block's earlier rows are rounded again at the
+ *                   new scale.  Elements are stored as e4m3(x / s), saturated.
+ *                   Copy-on-write copies the scales along
+ *                   (pkv_copy_block_scales).
+ *   k_inv_scale, v_inv_scale : E4M3 caches without block_scales, as pkv_write.
+ *   query_start   : device int32[num_seqs + 1], or NULL for one token per
+ *                   sequence (total_tokens == num_seqs).
+ *   max_query_len : >= every n_s (sets the grid).
+ *   rope          : host struct, or NULL for no rotation.
+ * Each new position's block must be this sequence's alone, as the allocator's
+ * appends leave it: two rows of a call must not write one block.
+ * A sequence with invalid lengths (ctx outside [0, max_blocks * T], n_s > ctx,
+ * n_s > max_query_len, ctx > max_position) writes nothing, gets NaN q_out rows
+ * and sets PKV_DEVICE_BAD_LENGTH; a table entry outside [0, num_blocks) leaves
+ * its tokens unwritten and sets PKV_DEVICE_BAD_TABLE.  Without query_start a
+ * sequence of context 0 writes nothing and gets a zero q_out row.  Rows outside
+ * [query_start[0], query_start[num_seqs]) and outside [0, total_tokens) are
+ * left alone.  Launched with programmatic stream serialization, like the
+ * tensor-core decode kernels; asynchronous on `stream`. */
+PKV_API pkv_status pkv_append(void* k_cache, void* v_cache, float* block_scales, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                              const void* q, int64_t q_stride, int32_t num_q_heads,
+                              int32_t src_dtype, const int32_t* block_tables, int32_t max_blocks,
+                              const int32_t* context_lens, const int32_t* query_start,
+                              int32_t num_seqs, int32_t total_tokens, int32_t max_query_len,
+                              const pkv_rope* rope, const pkv_kv_desc* desc, float k_inv_scale,
+                              float v_inv_scale, void* stream);
+
+/* The scales of copied blocks: what pkv_copy_blocks does for the bytes, for
+ * the block_scales of each layer (host array of num_layers <= 128 device
+ * pointers; src_dst as there). */
+PKV_API pkv_status pkv_copy_block_scales(float* const* block_scales, int32_t num_layers,
+                                         const int32_t* src_dst, int32_t n_pairs,
+                                         const pkv_kv_desc* desc, void* stream);
+
+/* ---------------------------------- sliding window, sinks, block scales
+ * Attention where a query sees a window of its context and a few first
+ * tokens: the query at position p sees p' iff
+ *   p' <= p and (p' > p - window_tokens or p' < sink_tokens).
+ * Table entries of blocks that no query of the call sees are not read, so
+ * those blocks may have gone back to the pool.  The block-scaled calls read
+ * an E4M3 cache as e4m3 * block_scales[block][KV head][K|V] (as pkv_append
+ * writes it; scales from 2^-40 to 2^40); with them window_tokens 0 means the
+ * whole context.  sink_tokens is ignored where nothing else is hidden. */
+
+/* Workspace bytes of the windowed and block-scaled decode calls for these
+ * sizes (0 if no split is needed). */
+PKV_API size_t pkv_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks,
+                                          const pkv_kv_desc* desc, int32_t window_tokens,
+                                          int32_t sink_tokens, int32_t partition_tokens);
+
+/* pkv_attention_decode over what the window leaves visible (window_tokens >=
+ * 1): arguments, workspace (of pkv_window_workspace_bytes), splits, launch and
+ * errors as there; the query of sequence s is at position context_lens[s] - 1.
+ * partition_tokens counts visible tokens, a multiple of 64 (0: automatic).
+ * The tensor-core kernel takes 16-bit caches and E4M3 caches with head_dim
+ * 128, the CUDA-core kernel the others; pkv_set_attention_kernel applies. */
+PKV_API pkv_status pkv_attention_decode_window(
+    void* out, const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens, int32_t num_seqs,
+    int32_t num_q_heads, const pkv_kv_desc* desc, int32_t window_tokens, int32_t sink_tokens,
+    float softmax_scale, float k_scale, float v_scale, int32_t partition_tokens, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* The same over a block-scaled E4M3 cache, with or without a window. */
+PKV_API pkv_status pkv_attention_decode_block_scaled(
+    void* out, const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+    const float* block_scales, const int32_t* block_tables, int32_t max_blocks,
+    const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, const pkv_kv_desc* desc,
+    int32_t window_tokens, int32_t sink_tokens, float softmax_scale, int32_t partition_tokens,
+    void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------- prefix caching
  * [C "The knobs"]: enable_prefix_caching hashes each filled block so that
  * unrelated requests share physical blocks; [C "Failure modes"]: sharing is

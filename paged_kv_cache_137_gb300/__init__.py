@@ -77,6 +77,11 @@ def with_head_scales(desc: pkv_kv_desc, head_scales) -> pkv_kv_desc:
                    head_scales)
 
 
+class pkv_rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32, _I64, _U64, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -129,6 +134,14 @@ _SIGNATURES = {
     "pkv_decode_step_shared_prefix": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32,
                                              _PDESC, _I32, _F, _F, _F, _F, _F, _I32, _P,
                                              ctypes.c_size_t, _P]),
+    "pkv_append": (_I32, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _I32, _P, _P, _I32,
+                          _I32, _I32, ctypes.POINTER(pkv_rope), _PDESC, _F, _F, _P]),
+    "pkv_copy_block_scales": (_I32, [ctypes.POINTER(_P), _I32, _PI32, _I32, _PDESC, _P]),
+    "pkv_window_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32, _PDESC, _I32, _I32, _I32]),
+    "pkv_attention_decode_window": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _P, _I32, _I32, _PDESC, _I32,
+                                           _I32, _F, _F, _F, _I32, _P, ctypes.c_size_t, _P]),
+    "pkv_attention_decode_block_scaled": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _I32, _P, _I32, _I32, _PDESC,
+                                                 _I32, _I32, _F, _I32, _P, ctypes.c_size_t, _P]),
     "pkv_device_status": (_I32, [_PI32, _I32, _P]),
     "pkv_set_stage_wait_limit": (_I32, [_U64]),
     "pkv_last_error": (ctypes.c_char_p, []),
@@ -742,6 +755,190 @@ def pkv_decode_step_shared_prefix(out, q, k_cache, v_cache, k_new, v_new, block_
                                  desc, prefix_blocks, softmax_scale, k_scale, v_scale, k_inv_scale,
                                  v_inv_scale, partition_tokens, workspace)
     _check(fn(*args, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------- append with rotation
+def rope_table(max_position, rotary_dim, base=10000.0, device="cuda") -> torch.Tensor:
+    """float32 [max_position, rotary_dim]: the cosines, then the sines, of the
+    angles p * base^(-2i / rotary_dim), computed in fp64 (the angle of a far
+    position needs more than fp32)."""
+    inv = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / max(rotary_dim, 1))
+    ang = torch.arange(max_position, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], dim=1).float().contiguous().to(device)
+
+
+def rope(cos_sin, interleaved=False) -> pkv_rope:
+    """The rotation of pkv_append: cos_sin float32 [max_position, rotary_dim]
+    (see rope_table), pairs (i, i + rotary_dim / 2) or, interleaved, (2i, 2i +
+    1).  Keeps a reference to the table."""
+    if (not isinstance(cos_sin, torch.Tensor) or not cos_sin.is_cuda or cos_sin.dtype != torch.float32
+            or cos_sin.dim() != 2 or not cos_sin.is_contiguous()):
+        raise ValueError("cos_sin must be a contiguous float32 CUDA tensor [max_position, rotary_dim]")
+    r = pkv_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)))
+    r._cos_sin = cos_sin
+    return r
+
+
+def empty_block_scales(desc: pkv_kv_desc, device="cuda") -> torch.Tensor:
+    """Zero-filled scales of a block-scaled E4M3 cache [num_blocks, N_kv, 2] (K, V)."""
+    return torch.zeros((desc.num_blocks, desc.num_kv_heads, 2), dtype=torch.float32, device=device)
+
+
+def _scales(block_scales, desc):
+    t = block_scales
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous()
+            or t.shape != (desc.num_blocks, desc.num_kv_heads, 2)):
+        raise ValueError("block_scales must be a contiguous float32 CUDA tensor [num_blocks, num_kv_heads, 2]")
+    return t.data_ptr()
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, n, heads, d):
+    """(address, elements between tokens) of [n, heads, d] whose tokens may lie
+    apart (a view of a packed projection)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.shape != (n, heads, d) or (n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}] with contiguous token rows")
+    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d)
+
+
+def _cache_args(k_cache, v_cache, desc):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or tuple(t.shape) != desc.cache_shape:
+            raise ValueError(f"{name} must be {desc.torch_dtype}{desc.cache_shape}")
+    return _dev(k_cache, "k_cache", desc.torch_dtype), _dev(v_cache, "v_cache", desc.torch_dtype)
+
+
+def _append_args(k_cache, v_cache, k, v, block_tables, context_lens, desc, query_start, max_query_len, rope,
+                 q, q_out, block_scales, k_inv_scale, v_inv_scale):
+    n, b = k.shape[0], context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.dim() != 1:
+        raise ValueError("block_tables int32[B, max_blocks], context_lens int32[B] expected")
+    if query_start is None:
+        if n != b:
+            raise ValueError("without query_start there is one token per sequence")
+        if max_query_len is not None and max_query_len < 1:
+            raise ValueError("max_query_len must be at least 1")
+        longest = 1
+    else:
+        if query_start.shape != (b + 1,):
+            raise ValueError("query_start must be int32[B + 1]")
+        longest = max_query_len
+        if longest is None:
+            longest = int((query_start[1:] - query_start[:-1]).max().item()) if b else 0
+    dtype = k.dtype
+    h, d = desc.num_kv_heads, desc.head_dim
+    kc, vc = _cache_args(k_cache, v_cache, desc)
+    kp, ks = _token_rows(k, "k", dtype, n, h, d)
+    vp, vs = _token_rows(v, "v", dtype, n, h, d)
+    qp, qs, op, hq = None, 0, None, 0
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _token_rows(q, "q", dtype, n, hq, d)
+        if q_out is None or q_out.shape != q.shape or q_out.dtype != dtype:
+            raise ValueError("q_out must match q")
+        op = _dev(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    return (kc, vc, None if block_scales is None else _scales(block_scales, desc), kp, ks, vp, vs, op, qp, qs, hq,
+            _dtype_code(k), _dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+            _dev(context_lens, "context_lens", torch.int32),
+            None if query_start is None else _dev(query_start, "query_start", torch.int32), b, n, int(longest),
+            None if rope is None else ctypes.byref(rope), ctypes.byref(desc), float(k_inv_scale),
+            float(v_inv_scale))
+
+
+def pkv_append(k_cache, v_cache, k, v, block_tables, context_lens, desc: pkv_kv_desc, query_start=None,
+               max_query_len=None, rope: pkv_rope | None = None, q=None, q_out=None, block_scales=None,
+               k_inv_scale=1.0, v_inv_scale=1.0, stream=None):
+    """Write each sequence's new tokens at its last positions, K and q rotated
+    by them (pkv_append).  k, v [n, N_kv, D] and q [n, Hq, D] may be views of a
+    packed projection; query_start int32[B + 1] gives each sequence's rows
+    (None: one token each).  Returns q_out."""
+    _check(lib().pkv_append(*_append_args(k_cache, v_cache, k, v, block_tables, context_lens, desc, query_start,
+                                          max_query_len, rope, q, q_out, block_scales, k_inv_scale,
+                                          v_inv_scale), _stream(stream)))
+    return q_out
+
+
+def prepare_append(k_cache, v_cache, k, v, block_tables, context_lens, desc: pkv_kv_desc, query_start=None,
+                   max_query_len=None, rope: pkv_rope | None = None, q=None, q_out=None, block_scales=None,
+                   k_inv_scale=1.0, v_inv_scale=1.0) -> Prepared:
+    """pkv_append on these buffers as a Prepared call."""
+    args = _append_args(k_cache, v_cache, k, v, block_tables, context_lens, desc, query_start, max_query_len,
+                        rope, q, q_out, block_scales, k_inv_scale, v_inv_scale)
+    return Prepared(lib().pkv_append, args, (k_cache, v_cache, k, v, block_tables, context_lens, desc,
+                                             query_start, rope, q, q_out, block_scales))
+
+
+def pkv_copy_block_scales(block_scales, src_dst, desc: pkv_kv_desc, stream=None):
+    """Copy the scales of blocks src -> dst of every layer (a list of
+    [num_blocks, N_kv, 2] tensors); src_dst is a host int32 [n, 2]."""
+    pairs = np.ascontiguousarray(np.asarray(src_dst, dtype=np.int32).reshape(-1))
+    if len(pairs) == 0:
+        return
+    ptrs = (_P * len(block_scales))(*[_scales(t, desc) for t in block_scales])
+    _check(lib().pkv_copy_block_scales(ptrs, len(block_scales), _i32p(pairs), len(pairs) // 2,
+                                       ctypes.byref(desc), _stream(stream)))
+
+
+# ------------------------------------- sliding window, sinks, block scales
+def pkv_window_workspace_bytes(num_seqs, num_q_heads, max_blocks, desc: pkv_kv_desc, window_tokens=0,
+                               sink_tokens=0, partition_tokens=0) -> int:
+    return int(lib().pkv_window_workspace_bytes(num_seqs, num_q_heads, max_blocks, ctypes.byref(desc),
+                                                int(window_tokens), int(sink_tokens), int(partition_tokens)))
+
+
+def window_workspace_for(num_seqs, num_q_heads, max_blocks, desc, window_tokens=0, sink_tokens=0,
+                         partition_tokens=0, device="cuda"):
+    """A zero-filled workspace for the windowed and block-scaled decode calls (None if 0)."""
+    n = pkv_window_workspace_bytes(num_seqs, num_q_heads, max_blocks, desc, window_tokens, sink_tokens,
+                                   partition_tokens)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc):
+    """The arguments up to the tables of the windowed and block-scaled calls,
+    checked: (out, q, dtype, k, v), (tables, max_blocks, lengths), sequences, heads."""
+    n, hq, d = q.shape
+    if out.shape != q.shape or out.dtype != q.dtype or d != desc.head_dim:
+        raise ValueError("out must match q [rows, Hq, head_dim]")
+    b = context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.dim() != 1:
+        raise ValueError("block_tables int32[B, max_blocks], context_lens int32[B] expected")
+    kc, vc = _cache_args(k_cache, v_cache, desc)
+    return ((_dev(out, "out"), _dev(q, "q"), _dtype_code(q), kc, vc),
+            (_dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+             _dev(context_lens, "context_lens", torch.int32)), b, hq)
+
+
+def pkv_attention_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, desc: pkv_kv_desc,
+                                window_tokens, sink_tokens, softmax_scale, k_scale=1.0, v_scale=1.0,
+                                partition_tokens=0, workspace=None, stream=None):
+    """Decode attention of q [B, Hq, D] over each context's last window_tokens
+    positions and its first sink_tokens (pkv_attention_decode_window); the
+    workspace is window_workspace_for's."""
+    head, tab, b, hq = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc)
+    if q.shape[0] != b:
+        raise ValueError("one query per sequence expected")
+    _check(lib().pkv_attention_decode_window(
+        *head, *tab, b, hq, ctypes.byref(desc), int(window_tokens), int(sink_tokens), float(softmax_scale),
+        float(k_scale), float(v_scale), int(partition_tokens), *_ws(workspace), _stream(stream)))
+    return out
+
+
+def pkv_attention_decode_block_scaled(out, q, k_cache, v_cache, block_scales, block_tables, context_lens,
+                                      desc: pkv_kv_desc, softmax_scale, window_tokens=0, sink_tokens=0,
+                                      partition_tokens=0, workspace=None, stream=None):
+    """Decode attention over an E4M3 cache with a scale per (block, KV head)
+    (pkv_attention_decode_block_scaled); window_tokens 0 sees the whole context."""
+    head, tab, b, hq = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc)
+    if q.shape[0] != b:
+        raise ValueError("one query per sequence expected")
+    _check(lib().pkv_attention_decode_block_scaled(
+        *head, _scales(block_scales, desc), *tab, b, hq, ctypes.byref(desc), int(window_tokens),
+        int(sink_tokens), float(softmax_scale), int(partition_tokens), *_ws(workspace), _stream(stream)))
     return out
 
 

@@ -275,6 +275,8 @@ int sizing_q_dtype(const pkv_kv_desc* d) { return d->kv_dtype == PKV_E4M3 ? PKV_
 
 }  // namespace
 
+int attention_kernel_choice() { return g_kernel_choice.load(); }
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;

@@ -121,6 +121,9 @@ pkv_status launch_write_last(void* k_cache, void* v_cache, const void* k_new, co
                              const int32_t* tables, int32_t max_blocks, const int32_t* ctx_lens,
                              int32_t num_seqs, const pkv_kv_desc* desc, cudaStream_t st);
 
+// Process-wide decode kernel choice (pkv_set_attention_kernel).
+int attention_kernel_choice();
+
 // Launch the CUDA-core decode kernel for one (cache dtype, q dtype) pair;
 // returns PKV_ERR_UNSUPPORTED for a shape it was not compiled for.
 template <typename KV, typename Q>

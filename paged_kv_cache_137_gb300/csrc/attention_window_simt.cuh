@@ -1,0 +1,160 @@
+// CUDA-core form of windowed and block-scaled decode attention: fp32 caches,
+// E4M3 caches with head_dim 64, and any other shape when the CUDA-core kernels
+// are asked for.  The same chunks, splits and merge as attention_window.cuh; a
+// warp takes every fourth chunk of its split, two lanes share a token in the
+// q.k phase (head_dim / 2 elements each) and the lanes split head_dim for
+// p.V.  All G heads (padded to GM) go together, so a K/V element is read once
+// per CTA.  The block's V scale multiplies p in fp32.
+#pragma once
+
+#include "attention_window.cuh"
+
+namespace pkv {
+
+template <typename KV, typename Q, int D, int GM>
+__global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const WindowArgs a) {
+  using namespace tc;
+  constexpr int DQ = D / 2, DV = D / 32, KCH = 8;
+  constexpr unsigned FULL = 0xffffffffu;
+  using raw = typename KV::raw;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int kvh = blockIdx.x, seq = blockIdx.y, split = blockIdx.z;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int G = a.group, T = a.block_size;
+  const int ctx = a.ctx_lens[seq];
+  const bool bad_ctx = ctx < 0 || ctx > a.max_blocks * T;
+  const Span span(bad_ctx ? 0 : ctx, a.window, a.sinks);
+  const int nsplit = max(1, (span.n + a.part_chunks - 1) / a.part_chunks);
+  if (split >= nsplit) return;
+  const HeadScales hs = head_scales(a.head_scales, a.num_kv_heads, kvh, a.softmax_scale, a.qk_scale,
+                                    a.v_scale, 1.f, 1.f);
+  const int64_t n_all = span.n;
+  const int c0 = static_cast<int>(split * n_all / nsplit);
+  const int c1 = static_cast<int>((split + 1) * n_all / nsplit);
+
+  __shared__ float q_s[GM][D];
+  __shared__ float p_s[kWarps][kChunk][GM];
+  __shared__ __align__(16) float merge_s[2 * kWarps * 16 + kWarps * 16 * D];
+  __shared__ int s_bad, s_last;
+  if (threadIdx.x == 0) s_bad = bad_ctx ? kBadLength : 0;
+  for (int i = threadIdx.x; i < GM * D; i += kThreads) {
+    const int j = i / D, d = i % D;
+    q_s[j][d] = j < G ? load_elem<Q>(a.q, (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + j) * D + d) * hs.qk
+                      : 0.f;
+  }
+  __syncthreads();
+
+  float m[GM], lsum[GM], acc[GM][DV];
+#pragma unroll
+  for (int j = 0; j < GM; ++j) {
+    m[j] = -CUDART_INF_F;
+    lsum[j] = 0.f;
+#pragma unroll
+    for (int e = 0; e < DV; ++e) acc[j][e] = 0.f;
+  }
+  const int tok = lane % kChunk, part = lane / kChunk;
+  bool bad = false;
+  for (int c = c0 + warp; c < c1; c += kWarps) {
+    const int pos = span.chunk(c) * kChunk;
+    const int blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + pos / T];
+    if (blk < 0 || blk >= a.num_blocks) {   // the same for the whole warp
+      bad = true;
+      break;
+    }
+    const size_t slab = static_cast<size_t>(blk) * a.num_kv_heads + kvh;
+    const size_t base = (slab * T + pos % T) * D;
+    float ks = 1.f, vs = 1.f;
+    if (a.block_scales) {
+      ks = a.block_scales[2 * slab];
+      vs = a.block_scales[2 * slab + 1];
+    }
+    float s[GM];
+#pragma unroll
+    for (int j = 0; j < GM; ++j) s[j] = 0.f;
+    const raw* kp = static_cast<const raw*>(a.k_cache) + base + static_cast<size_t>(tok) * D + part * DQ;
+#pragma unroll (GM > 4 ? 1 : 4)
+    for (int d0 = 0; d0 < DQ; d0 += KCH) {
+      float kf[KCH];
+      LoadF32<KV, KCH>::run(kp + d0, kf);
+#pragma unroll
+      for (int j = 0; j < GM; ++j)
+#pragma unroll
+        for (int e = 0; e < KCH; ++e) s[j] = fmaf(q_s[j][part * DQ + d0 + e], kf[e], s[j]);
+    }
+    const bool seen = span.sees(pos + tok);
+    float corr[GM];
+#pragma unroll
+    for (int j = 0; j < GM; ++j) {
+      s[j] += __shfl_xor_sync(FULL, s[j], kChunk);
+      const float sj = seen ? s[j] * ks : -CUDART_INF_F;
+      float bm = sj;
+#pragma unroll
+      for (int off = 1; off < kChunk; off <<= 1) bm = fmaxf(bm, __shfl_xor_sync(FULL, bm, off));
+      const float mn = fmaxf(m[j], bm), ref = finite_or_0(mn);
+      const float p = exp2f(sj - ref);
+      float ps = p;
+#pragma unroll
+      for (int off = 1; off < kChunk; off <<= 1) ps += __shfl_xor_sync(FULL, ps, off);
+      corr[j] = exp2f(m[j] - ref);
+      lsum[j] = lsum[j] * corr[j] + ps;
+      m[j] = mn;
+      if (part == 0) p_s[warp][tok][j] = p * vs;
+    }
+#pragma unroll
+    for (int j = 0; j < GM; ++j)
+#pragma unroll
+      for (int e = 0; e < DV; ++e) acc[j][e] *= corr[j];
+    __syncwarp();
+    const raw* vp = static_cast<const raw*>(a.v_cache) + base + lane * DV;
+#pragma unroll 4
+    for (int t = 0; t < kChunk; ++t) {
+      if (!span.sees(pos + t)) continue;   // what an unseen row holds is never read
+      float vf[DV];
+      LoadF32<KV, DV>::run(vp + static_cast<size_t>(t) * D, vf);
+#pragma unroll
+      for (int j = 0; j < GM; ++j) {
+        const float pj = p_s[warp][t][j];
+#pragma unroll
+        for (int e = 0; e < DV; ++e) acc[j][e] = fmaf(pj, vf[e], acc[j][e]);
+      }
+    }
+    __syncwarp();
+  }
+  if (bad && lane == 0) atomicOr(&s_bad, kBadTable);
+  float* mS = merge_s;
+  float* lS = mS + kWarps * 16;
+  float* oS = lS + kWarps * 16;
+#pragma unroll
+  for (int j = 0; j < GM; ++j) {
+    if (lane == 0) {
+      mS[warp * 16 + j] = lsum[j] == lsum[j] ? m[j] : 0.f;   // a NaN sum reaches the merge
+      lS[warp * 16 + j] = lsum[j];
+    }
+#pragma unroll
+    for (int e = 0; e < DV; ++e) oS[(warp * 16 + j) * D + lane * DV + e] = acc[j][e];
+  }
+  __syncthreads();
+  finish_unit<Q, D>(a, mS, lS, oS, kvh, seq, split, nsplit, s_bad, hs.v, merge_s,
+                    static_cast<int>(sizeof(merge_s) / sizeof(float)), &s_last);
+}
+
+template <typename KV, typename Q, int D>
+pkv_status launch_window_simt_d(const WindowArgs& a, cudaStream_t st) {
+  const dim3 grid(a.num_kv_heads, a.num_seqs, a.max_splits);
+  cudaError_t e;
+  if (a.group <= 1) e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 1>, grid, tc::kThreads, 0, st, a);
+  else if (a.group <= 4) e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 4>, grid, tc::kThreads, 0, st, a);
+  else if (a.group <= 8) e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 8>, grid, tc::kThreads, 0, st, a);
+  else e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 16>, grid, tc::kThreads, 0, st, a);
+  if (e != cudaSuccess) return cuda_fail("windowed decode: launch", e);
+  return check_launch("windowed decode (CUDA cores)");
+}
+
+template <typename KV, typename Q>
+pkv_status launch_window_simt(const WindowArgs& a, int head_dim, cudaStream_t st) {
+  if (head_dim == 128) return launch_window_simt_d<KV, Q, 128>(a, st);
+  if (head_dim == 64) return launch_window_simt_d<KV, Q, 64>(a, st);
+  return fail(PKV_ERR_UNSUPPORTED, "windowed decode: head_dim not compiled");
+}
+
+}  // namespace pkv

@@ -621,6 +621,31 @@ PKV_API pkv_status pkv_attention_decode_block_scaled(
     int32_t window_tokens, int32_t sink_tokens, float softmax_scale, int32_t partition_tokens,
     void* workspace, size_t workspace_bytes, void* stream);
 
+/* pkv_attention_prefill over what the window leaves visible (window_tokens >=
+ * 1; each query by its own position): arguments, layout, launch and errors as
+ * there.  Runs on tcgen05 for every cache it takes, 16-bit with head_dim 64 or
+ * 128 and E4M3 with head_dim 128, whatever the sign of softmax_scale;
+ * pkv_set_prefill_kernel does not apply.  A NaN or an infinity in V at a
+ * position that one query of the call sees can reach the others of its KV
+ * head's 256 rows (a weight of 0 times it is NaN), as in pkv_attention_prefill. */
+PKV_API pkv_status pkv_attention_prefill_window(
+    void* out, const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
+    const int32_t* query_start, int32_t num_seqs, int32_t total_q, int32_t max_query_len,
+    int32_t num_q_heads, const pkv_kv_desc* desc, int32_t window_tokens, int32_t sink_tokens,
+    float softmax_scale, float k_scale, float v_scale, void* stream);
+
+/* The same over a block-scaled E4M3 cache, with or without a window.  Scales
+ * that are no powers of two cost a value up to 2^-10 of itself (they meet f16
+ * products); a value is off by up to 2^-24 of the largest scale among its 64
+ * neighbours where the scales differ by more than 2^15 there. */
+PKV_API pkv_status pkv_attention_prefill_block_scaled(
+    void* out, const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+    const float* block_scales, const int32_t* block_tables, int32_t max_blocks,
+    const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs, int32_t total_q,
+    int32_t max_query_len, int32_t num_q_heads, const pkv_kv_desc* desc, int32_t window_tokens,
+    int32_t sink_tokens, float softmax_scale, void* stream);
+
 /* ---------------------------------------------------------- prefix caching
  * [C "The knobs"]: enable_prefix_caching hashes each filled block so that
  * unrelated requests share physical blocks; [C "Failure modes"]: sharing is

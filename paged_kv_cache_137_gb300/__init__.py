@@ -142,6 +142,10 @@ _SIGNATURES = {
                                            _I32, _F, _F, _F, _I32, _P, ctypes.c_size_t, _P]),
     "pkv_attention_decode_block_scaled": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _I32, _P, _I32, _I32, _PDESC,
                                                  _I32, _I32, _F, _I32, _P, ctypes.c_size_t, _P]),
+    "pkv_attention_prefill_window": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                                            _PDESC, _I32, _I32, _F, _F, _F, _P]),
+    "pkv_attention_prefill_block_scaled": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32,
+                                                  _I32, _PDESC, _I32, _I32, _F, _P]),
     "pkv_device_status": (_I32, [_PI32, _I32, _P]),
     "pkv_set_stage_wait_limit": (_I32, [_U64]),
     "pkv_last_error": (ctypes.c_char_p, []),
@@ -939,6 +943,43 @@ def pkv_attention_decode_block_scaled(out, q, k_cache, v_cache, block_scales, bl
     _check(lib().pkv_attention_decode_block_scaled(
         *head, _scales(block_scales, desc), *tab, b, hq, ctypes.byref(desc), int(window_tokens),
         int(sink_tokens), float(softmax_scale), int(partition_tokens), *_ws(workspace), _stream(stream)))
+    return out
+
+
+def _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, desc, max_query_len):
+    head, tab, b, hq = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc)
+    if query_start.shape != (b + 1,):
+        raise ValueError("query_start must be int32[B + 1]")
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if b else 0
+    return head, (*tab, _dev(query_start, "query_start", torch.int32), b, q.shape[0], int(max_query_len), hq,
+                  ctypes.byref(desc))
+
+
+def pkv_attention_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                                 desc: pkv_kv_desc, window_tokens, sink_tokens, softmax_scale,
+                                 max_query_len=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """Prefill attention of packed chunks q [total_q, Hq, D], each query over
+    its last window_tokens positions and the first sink_tokens
+    (pkv_attention_prefill_window); otherwise as pkv_attention_prefill."""
+    head, rest = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, desc,
+                               max_query_len)
+    _check(lib().pkv_attention_prefill_window(
+        *head, *rest, int(window_tokens), int(sink_tokens), float(softmax_scale), float(k_scale),
+        float(v_scale), _stream(stream)))
+    return out
+
+
+def pkv_attention_prefill_block_scaled(out, q, k_cache, v_cache, block_scales, block_tables, context_lens,
+                                       query_start, desc: pkv_kv_desc, softmax_scale, max_query_len=None,
+                                       window_tokens=0, sink_tokens=0, stream=None):
+    """Prefill attention over an E4M3 cache with a scale per (block, KV head)
+    (pkv_attention_prefill_block_scaled); window_tokens 0 sees the whole context."""
+    head, rest = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, desc,
+                               max_query_len)
+    _check(lib().pkv_attention_prefill_block_scaled(
+        *head, _scales(block_scales, desc), *rest, int(window_tokens), int(sink_tokens), float(softmax_scale),
+        _stream(stream)))
     return out
 
 

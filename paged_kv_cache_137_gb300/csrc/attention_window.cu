@@ -210,7 +210,6 @@ pkv_status decode_window_impl(void* out, const void* q, int32_t q_dtype, const v
 
 }  // namespace
 
-// The checks a cache with block scales adds.
 pkv_status check_block_scales(const pkv_kv_desc* desc, const float* block_scales) {
   if (desc->kv_dtype != PKV_E4M3) return fail(PKV_ERR_INVALID_ARG, "block_scales need an E4M3 cache");
   if (desc->head_scales)

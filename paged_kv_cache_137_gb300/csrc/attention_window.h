@@ -25,7 +25,19 @@ pkv_status launch_window_tc(const WindowArgs& a, int head_dim, const CUtensorMap
 template <typename KV, typename Q>
 pkv_status launch_window_simt(const WindowArgs& a, int head_dim, cudaStream_t st);
 
-// Resident CTAs per SM of the tensor-core kernel.
+// Prefill with a window, sinks or block scales (attention_window_prefill.cuh).
+struct WindowPrefillArgs : PrefillArgs {
+  int32_t window, sinks, block_size;
+  const float* block_scales;
+};
+template <typename KV, typename Q>
+pkv_status launch_window_prefill(const WindowPrefillArgs& a, int head_dim, int32_t max_query_len,
+                                 const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t st);
+
+// The checks a cache with block scales adds.
+pkv_status check_block_scales(const pkv_kv_desc* desc, const float* block_scales);
+
+// Resident CTAs per SM of the tensor-core decode kernel.
 int window_ctas_per_sm(const pkv_kv_desc* d, int group);
 
 }  // namespace pkv

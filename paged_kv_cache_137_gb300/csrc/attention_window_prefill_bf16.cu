@@ -1,0 +1,7 @@
+// Instantiation of windowed prefill attention: BF16 cache, BF16 queries.
+#include "attention_window_prefill.cuh"
+
+namespace pkv {
+template pkv_status launch_window_prefill<BF16, BF16>(const WindowPrefillArgs&, int, int32_t,
+                                                    const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+}  // namespace pkv

@@ -1,0 +1,7 @@
+// Instantiation of windowed prefill attention: E4M3 cache, F16 queries.
+#include "attention_window_prefill.cuh"
+
+namespace pkv {
+template pkv_status launch_window_prefill<E4M3, F16>(const WindowPrefillArgs&, int, int32_t,
+                                                    const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+}  // namespace pkv

@@ -108,6 +108,50 @@ __device__ __forceinline__ float clamp_scale(float x) {
   return fminf(fmaxf(x, 9.094947017729282e-13f), 1099511627776.f);   // 2^-40, 2^40
 }
 
+// The MMA warp runs its loop with all lanes and predicates each instruction on
+// one elected lane: inside a one-lane branch the operands' uniform registers
+// would be filled anew before every MMA, which measured about 100 cycles an
+// instruction and bound the whole pipeline.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p;
+}
+// D[tmem] (+)= A[smem] x B[smem], issued where `leader`.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem].
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+
 template <typename KV, typename Q, int D, bool BS>
 __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
     prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap kmap,
@@ -304,53 +348,56 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
-      const uint64_t k_desc = sw128_desc(smem_u32(kv16), 16, 1024);
-      const uint64_t v_desc = sw128_desc(smem_u32(kv16 + S_::kTile16), kSlab, 1024);
-      auto qk = [&](int X, int t) -> bool {
-        const int slot = t % kBuf, b = t & 1, i = 2 * X + b;
-        if (!mbar_wait(smem_u32(kFp8 ? &conv_full[slot] : &full[slot]), (t / kBuf) & 1, kWaitNs)) return false;
-        // the buffer's step t - 2: its P has been read by P V
-        if (t >= 2 && !mbar_wait(smem_u32(&o_done[i]), ((t >> 1) - 1) & 1, kWaitNs)) return false;
-        tc_fence_after();
-        const uint64_t qd = q_desc + ((X * S_::kQTile) >> 4);
-        const uint64_t kd = k_desc + ((slot * S_::kStage16) >> 4);
-        const uint32_t d_tmem = tmem + 256 * X + 64 * b;
+    const uint32_t leader = elect_one();
+    const uint32_t tm = __reduce_max_sync(FULL, tmem);   // uniform for the compiler as well
+    const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
+    const uint64_t k_desc = sw128_desc(smem_u32(kv16), 16, 1024);
+    const uint64_t v_desc = sw128_desc(smem_u32(kv16 + S_::kTile16), kSlab, 1024);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(FULL, mbar_wait(smem_u32(bar), parity, kWaitNs));
+    };
+    auto qk = [&](int X, int t) -> bool {
+      const int slot = t % kBuf, b = t & 1, i = 2 * X + b;
+      if (!wait(kFp8 ? &conv_full[slot] : &full[slot], (t / kBuf) & 1)) return false;
+      // the buffer's step t - 2: its P has been read by P V
+      if (t >= 2 && !wait(&o_done[i], ((t >> 1) - 1) & 1)) return false;
+      tc_fence_after();
+      const uint64_t qd = q_desc + ((X * S_::kQTile) >> 4);
+      const uint64_t kd = k_desc + ((slot * S_::kStage16) >> 4);
+      const uint32_t d_tmem = tm + 256 * X + 64 * b;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma::umma(d_tmem, qd + (((ks >> 2) * kQSlab + 32 * (ks & 3)) >> 4),
-                     kd + (((ks >> 2) * kSlab + 32 * (ks & 3)) >> 4), kIdQK, ks > 0 ? 1u : 0u);
-        umma_commit(smem_u32(&s_full[i]));
-        return true;
-      };
-      auto pv = [&](int X, int t) -> bool {
-        const int b = t & 1, i = 2 * X + b;
-        if (!mbar_wait(smem_u32(&p_full[i]), (t >> 1) & 1, kWaitNs)) return false;
-        tc_fence_after();
-        const uint64_t vd = v_desc + (((t % kBuf) * S_::kStage16) >> 4);
-        const uint32_t d_tmem = tmem + 256 * X + 128, p_tmem = tmem + 256 * X + 64 * b;
+      for (int ks = 0; ks < D / 16; ++ks)
+        mma_ss(leader, d_tmem, qd + (((ks >> 2) * kQSlab + 32 * (ks & 3)) >> 4),
+               kd + (((ks >> 2) * kSlab + 32 * (ks & 3)) >> 4), kIdQK, ks > 0 ? 1u : 0u);
+      commit(leader, smem_u32(&s_full[i]));
+      return true;
+    };
+    auto pv = [&](int X, int t) -> bool {
+      const int b = t & 1, i = 2 * X + b;
+      if (!wait(&p_full[i], (t >> 1) & 1)) return false;
+      tc_fence_after();
+      const uint64_t vd = v_desc + (((t % kBuf) * S_::kStage16) >> 4);
+      const uint32_t d_tmem = tm + 256 * X + 128, p_tmem = tm + 256 * X + 64 * b;
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_ts(d_tmem, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (t > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(smem_u32(&o_done[i]));
-        return true;
-      };
-      bool ok = true;
-      for (int t = 0; t < 2 && ok; ++t)
-        for (int X = 0; X < 2 && ok; ++X)
-          if (t < nt[X]) ok = qk(X, t);
-      for (int t = 0; t < steps && ok; ++t) {
-        for (int X = 0; X < 2 && ok; ++X)
-          if (t < nt[X]) ok = pv(X, t);
-        if (!ok) break;
-        umma_commit(smem_u32(kFp8 ? &wide_free[t % kBuf] : &empty[t % kBuf]));
-        for (int X = 0; X < 2 && ok; ++X)
-          if (t + 2 < nt[X]) ok = qk(X, t + 2);
-      }
-      if (!ok) atomicOr(&s_bad, kTimeout);
-      umma_commit(smem_u32(&fin));
+      for (int kk = 0; kk < kKeys / 16; ++kk)
+        mma_ts(leader, d_tmem, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (t > 0 || kk > 0) ? 1u : 0u);
+      commit(leader, smem_u32(&o_done[i]));
+      return true;
+    };
+    bool ok = true;
+    for (int t = 0; t < 2 && ok; ++t)
+      for (int X = 0; X < 2 && ok; ++X)
+        if (t < nt[X]) ok = qk(X, t);
+    for (int t = 0; t < steps && ok; ++t) {
+      for (int X = 0; X < 2 && ok; ++X)
+        if (t < nt[X]) ok = pv(X, t);
+      if (!ok) break;
+      commit(leader, smem_u32(kFp8 ? &wide_free[t % kBuf] : &empty[t % kBuf]));
+      for (int X = 0; X < 2 && ok; ++X)
+        if (t + 2 < nt[X]) ok = qk(X, t + 2);
     }
+    if (!ok && lane == 0) atomicOr(&s_bad, kTimeout);
+    commit(leader, smem_u32(&fin));
   } else if (kFp8 && warp >= kConvWarp) {
     // ------------------------------------------------------------ converters
     // two warps K, two V; each half of the 64 rows, a 16-byte piece (16

@@ -56,11 +56,12 @@ using namespace umma;
 
 constexpr int kChunkKeys = 16;
 constexpr int kStepChunks = kKeys / kChunkKeys;   // 4
-constexpr int kWide = 3;                          // widened 16-bit buffers (E4M3)
 constexpr int kUnitRows = 2 * kRows;              // query rows of a unit
-// warps: 0-7 softmax (four a tile), TMA, MMA of tile A and B, scheduler, converters
-constexpr int kProdWarp = 8, kMmaWarp = 9, kSchedWarp = 11, kConvWarp = 12, kConvWarps = 4;
-constexpr int kScaleRing = 8;
+// warps: 0-7 softmax (four a tile), TMA, MMA of tile A and B, scheduler, four helpers
+constexpr int kProdWarp = 8, kMmaWarp = 9, kSchedWarp = 11, kHelpWarp = 12;
+constexpr int kThreadsW = 512;
+constexpr int kWideK = 2, kWideV = 3;             // widened K and V buffers (E4M3)
+constexpr int kScaleRing = 16;                    // steps whose scales are kept: more than are in flight
 
 // What the 256 rows of a unit see: positions [0, sinks) and [w0, last], as
 // chunks of 16; the first ns chunks, then those from wb on, n in all.
@@ -89,13 +90,15 @@ struct Shape {
   static constexpr int kSlabs = D / 64;                     // 128-byte slabs of a 16-bit row
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kTile16 = kKeys * D * 2;             // K (or V) of a step, 16 bits
-  static constexpr int kStage16 = 2 * kTile16;
-  static constexpr int kTile8 = kKeys * D;
-  static constexpr int kStage8 = 2 * kTile8;
-  static constexpr int kRing = kFp8 ? 4 : 5;                // TMA stages
-  static constexpr int kRingBytes = kFp8 ? kRing * kStage8 + kWide * kStage16 : kRing * kStage16;
-  static constexpr int kSmem = 1024 + 2 * kQTile + kRingBytes;
-  static constexpr int kThreads = 32 * (kFp8 ? kConvWarp + kConvWarps : kConvWarp);
+  static constexpr int kTile = kKeys * D * KV::bytes;       // as it is stored
+  static constexpr int kStage = 2 * kTile;                  // K, then V
+  static constexpr int kRing = 5;                           // TMA stages
+  static constexpr int kWideBytes = kFp8 ? (kWideK + kWideV) * kTile16 : 0;
+  static constexpr int kSmem = 1024 + 2 * kQTile + kRing * kStage + kWideBytes;
+  // 16-bit K and V of a step as the MMAs see them: the ring's stages, or the
+  // widened buffers
+  static constexpr int kBufK = kFp8 ? kWideK : kRing, kBufV = kFp8 ? kWideV : kRing;
+  static constexpr int kStrideK = kFp8 ? kTile16 : kStage, kStrideV = kStrideK;
 };
 
 using Args = WindowPrefillArgs;
@@ -126,9 +129,8 @@ struct Unit {
     steps = max(nt[0], nt[1]);
   }
   __device__ __forceinline__ int pos_of(int r, int G) const { return first + (row0 + r) / G; }
-  // element offset of row r in q and out
-  __device__ __forceinline__ int64_t row_at(int r, const Args& a, int D) const {
-    const int i = (row0 + r) / a.group, j = row0 + r - i * a.group;
+  // element offset of head j of chunk position i in q and out
+  __device__ __forceinline__ int64_t at(int i, int j, const Args& a, int D) const {
     return ((static_cast<int64_t>(q0) + i) * a.num_q_heads + kvh * a.group + j) * D;
   }
 };
@@ -167,6 +169,28 @@ __device__ __forceinline__ int claimed_block(const ulonglong2& answer) {
       : "=r"(ok), "+r"(x)
       : "l"(answer.x), "l"(answer.y));
   return ok ? static_cast<int>(x) : -1;
+}
+
+// Two fp32 operations in one instruction, and the largest of three.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // The MMA warp runs its loop with all lanes and predicates each instruction on
@@ -214,7 +238,7 @@ __device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
 }
 
 template <typename KV, typename Q, int D, bool BS>
-__global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
+__global__ void __launch_bounds__(kThreadsW, 1)
     prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap) {
   using S_ = Shape<KV, D>;
@@ -225,9 +249,8 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
   constexpr uint32_t kIdPV = idesc(kBf, kRows, D, true);
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int kQSlab = kRows * 128;
-  constexpr int kBuf = kFp8 ? kWide : S_::kRing;            // 16-bit K/V buffers
-  // warps that read a unit's description: softmax, TMA, MMA, converters
-  constexpr int kReaders = 8 + 1 + 2 + (kFp8 ? kConvWarps : 0);
+  constexpr int kRing = S_::kRing, kBufK = S_::kBufK, kBufV = S_::kBufV;
+  constexpr int kReaders = 15;   // warps that read a unit's description: all but the scheduler
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, T = a.block_size;
@@ -235,28 +258,35 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* q_s = smem;                             // [tile][slab][128 rows][128 B]
-  uint8_t* ring = smem + 2 * S_::kQTile;           // 16-bit: [stage][K, V][slab]; E4M3: [stage][K, V]
-  uint8_t* wide = ring + S_::kRing * S_::kStage8;  // E4M3: widened [buffer][K, V][slab]
-  uint8_t* kv16 = kFp8 ? wide : ring;
-  __shared__ uint64_t full[S_::kRing], empty[S_::kRing], conv_full[kWide], wide_free[kWide];
-  __shared__ uint64_t q_full[2], s_full[4], p_full[4], o_done[4], o_free[2], fin;
+  uint8_t* ring = smem + 2 * S_::kQTile;           // [stage][K, V](16-bit: [slab])
+  uint8_t* wide = ring + kRing * S_::kStage;       // E4M3: widened K buffers, then V's
+  uint8_t* k16 = kFp8 ? wide : ring;
+  uint8_t* v16 = kFp8 ? wide + kWideK * S_::kTile16 : ring + S_::kTile;
+  __shared__ uint64_t full[kRing], empty[kRing];
+  __shared__ uint64_t k_full[kWideK], k_free[kWideK], v_full[kWideV], v_free[kWideV];   // E4M3
+  __shared__ uint64_t q_full[2], q_free[2], s_full[4], p_full[4], o_done[4], o_free[2], l_full[2], fin;
   __shared__ uint64_t work_full[2], work_empty[2], claim_bar;
   __shared__ ulonglong2 s_answer;
   __shared__ Work s_work[2];
-  __shared__ uint32_t s_ratio[BS ? kScaleRing : 1][2 * kStepChunks];   // half2 pairs: K, then V chunks
+  __shared__ __half s_ratio[BS ? kScaleRing : 1][2 * kStepChunks];   // scale / R: K, then V chunks
   __shared__ float s_ref[BS ? kScaleRing : 1][2];                      // R of K and V
+  __shared__ float s_inv[2][kRows];                                    // 1 / l of a finished row
   __shared__ uint32_t tmem_slot;
   __shared__ int s_timeout, s_issued, s_finished, s_claimed;
 
   if (tid == 0) {
     s_timeout = s_issued = s_finished = s_claimed = 0;
-    for (int i = 0; i < S_::kRing; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), kFp8 ? kConvWarps : 2);   // converters, or both MMA warps
+      mbar_init(smem_u32(&empty[i]), kFp8 ? 4 : 2);   // the helper warps, or both MMA warps
     }
-    for (int i = 0; i < kWide; ++i) {
-      mbar_init(smem_u32(&conv_full[i]), kConvWarps);
-      mbar_init(smem_u32(&wide_free[i]), 2);
+    for (int i = 0; i < kWideK; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 2);   // the two warps that widen K
+      mbar_init(smem_u32(&k_free[i]), 2);   // both MMA warps
+    }
+    for (int i = 0; i < kWideV; ++i) {
+      mbar_init(smem_u32(&v_full[i]), 2);
+      mbar_init(smem_u32(&v_free[i]), 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
@@ -265,7 +295,9 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&q_full[i]), kRows);
+      mbar_init(smem_u32(&q_free[i]), 1);
       mbar_init(smem_u32(&o_free[i]), kRows);
+      mbar_init(smem_u32(&l_full[i]), kRows);
       mbar_init(smem_u32(&work_full[i]), 1);
       mbar_init(smem_u32(&work_empty[i]), kReaders);
     }
@@ -424,8 +456,8 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
           sc_cur = sc_nxt;
           fetch(t / 8 + 1, row_nxt, sc_nxt);
         }
-        const int slot = g % S_::kRing;
-        if (g >= S_::kRing && !wait(&empty[slot], ((g / S_::kRing) - 1) & 1)) {
+        const int slot = g % kRing;
+        if (g >= kRing && !wait(&empty[slot], ((g / kRing) - 1) & 1)) {
           give_up();
           ok = false;
           break;
@@ -441,8 +473,7 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
           top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
           const float ref = top > 0.f ? pow2_floor(top) : 1.f;
           if (lane < 2 * kStepChunks) {
-            const __half2 h = __float2half2_rn(__fdividef(x, ref));
-            s_ratio[g % kScaleRing][lane] = *reinterpret_cast<const uint32_t*>(&h);
+            s_ratio[g % kScaleRing][lane] = __float2half_rn(__fdividef(x, ref));
             if ((lane & 3) == 0) s_ref[g % kScaleRing][lane >> 2] = ref;
           }
         }
@@ -453,8 +484,7 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
           mbar_arrive_expect_tx(bar, __popc(boxes) * static_cast<uint32_t>(kChunkKeys * 128));
         __syncwarp();
         if (load) {
-          uint8_t* dst = ring + slot * (kFp8 ? S_::kStage8 : S_::kStage16) +
-                         bv * (kFp8 ? S_::kTile8 : S_::kTile16) + bsl * kSlab + bc * (kChunkKeys * 128);
+          uint8_t* dst = ring + slot * S_::kStage + bv * S_::kTile + bsl * kSlab + bc * (kChunkKeys * 128);
           tma_load_2d(smem_u32(dst), bv ? &vmap : &kmap, bsl * 128, row, bar);
         }
         if (lane == 0) s_issued = g + 1;
@@ -468,10 +498,8 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
     const uint32_t leader = elect_one();
     const uint32_t tm = __reduce_max_sync(FULL, tmem) + 256 * X;   // uniform for the compiler as well
     const uint64_t q_desc = sw128_desc(smem_u32(q_s + X * S_::kQTile), 16, 1024);
-    const uint64_t k_desc = sw128_desc(smem_u32(kv16), 16, 1024);
-    const uint64_t v_desc = sw128_desc(smem_u32(kv16 + S_::kTile16), kSlab, 1024);
-    uint64_t* kv_full = kFp8 ? conv_full : full;
-    uint64_t* kv_free = kFp8 ? wide_free : empty;
+    const uint64_t k_desc = sw128_desc(smem_u32(k16), 16, 1024);
+    const uint64_t v_desc = sw128_desc(smem_u32(v16), kSlab, 1024);
     int g = 0, c = 0, units = 0;   // stream steps, this tile's steps and units so far
     bool ok = true;
     Work w;
@@ -480,33 +508,36 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
       release_work(k);
       const int nt = X ? u.nt[1] : u.nt[0];
       auto qk = [&](int t) -> bool {
-        const int slot = (g + t) % kBuf, i = 2 * X + ((c + t) & 1), use = (c + t) >> 1;
-        if (!wait(&kv_full[slot], ((g + t) / kBuf) & 1)) return false;
+        const int slot = (g + t) % kBufK, i = 2 * X + ((c + t) & 1), use = (c + t) >> 1;
+        if (!wait(kFp8 ? &k_full[slot] : &full[slot], ((g + t) / kBufK) & 1)) return false;
         // the buffer's step before: its P has been read by P V
         if (use >= 1 && !wait(&o_done[i], (use - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t kd = k_desc + ((slot * S_::kStage16) >> 4);
+        const uint64_t kd = k_desc + ((slot * S_::kStrideK) >> 4);
         const uint32_t d_tmem = tm + 64 * ((c + t) & 1);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           mma_ss(leader, d_tmem, q_desc + (((ks >> 2) * kQSlab + 32 * (ks & 3)) >> 4),
                  kd + (((ks >> 2) * kSlab + 32 * (ks & 3)) >> 4), kIdQK, ks > 0 ? 1u : 0u);
         commit(leader, smem_u32(&s_full[i]));
+        if (kFp8) commit(leader, smem_u32(&k_free[slot]));
+        if (t == nt - 1) commit(leader, smem_u32(&q_free[X]));
         return true;
       };
       auto pv = [&](int t) -> bool {
-        const int slot = (g + t) % kBuf, i = 2 * X + ((c + t) & 1);
+        const int slot = (g + t) % kBufV, i = 2 * X + ((c + t) & 1);
+        if (kFp8 && !wait(&v_full[slot], ((g + t) / kBufV) & 1)) return false;
         if (!wait(&p_full[i], ((c + t) >> 1) & 1)) return false;
         // O of the unit before has been read
         if (t == 0 && units > 0 && !wait(&o_free[X], (units - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t vd = v_desc + ((slot * S_::kStage16) >> 4);
+        const uint64_t vd = v_desc + ((slot * S_::kStrideV) >> 4);
         const uint32_t p_tmem = tm + 64 * ((c + t) & 1);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
           mma_ts(leader, tm + 128, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (t > 0 || kk > 0) ? 1u : 0u);
         commit(leader, smem_u32(&o_done[i]));
-        commit(leader, smem_u32(&kv_free[slot]));
+        commit(leader, smem_u32(kFp8 ? &v_free[slot] : &empty[slot]));
         return true;
       };
       if (nt > 0) {
@@ -516,106 +547,59 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
       }
       // the stream's steps that only the other tile reads
       for (int t = nt; t < u.steps && ok; ++t) {
-        const int slot = (g + t) % kBuf;
-        ok = wait(&kv_full[slot], ((g + t) / kBuf) & 1);
-        if (ok && lane == 0) mbar_arrive(smem_u32(&kv_free[slot]));
+        if constexpr (kFp8) {
+          const int sk = (g + t) % kBufK, sv = (g + t) % kBufV;
+          ok = wait(&k_full[sk], ((g + t) / kBufK) & 1) && wait(&v_full[sv], ((g + t) / kBufV) & 1);
+          if (ok && lane == 0) {
+            mbar_arrive(smem_u32(&k_free[sk]));
+            mbar_arrive(smem_u32(&v_free[sv]));
+          }
+        } else {
+          const int slot = (g + t) % kRing;
+          ok = wait(&full[slot], ((g + t) / kRing) & 1);
+          if (ok && lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+        }
       }
       if (!ok) give_up();
       g += u.steps;
       c += nt;
     }
     commit(leader, smem_u32(&fin));
-  } else if (kFp8 && warp >= kConvWarp) {
-    // ------------------------------------------------------------ converters
-    // two warps K, two V; each half of the 64 rows, a 16-byte piece (16
-    // elements) a lane at a time
-    const int cw = warp - kConvWarp, tv = cw >> 1, half = cw & 1;
-    int g = 0;
-    bool ok = true;
-    Work w;
-    for (int k = 0; ok && next_work(k, w); ++k) {
-      const Unit u(w, a);
-      release_work(k);
-      for (int t = 0; t < u.steps; ++t, ++g) {
-        const int slot = g % S_::kRing, b = g % kWide;
-        if (!wait(&full[slot], (g / S_::kRing) & 1) ||
-            (g >= kWide && !wait(&wide_free[b], ((g / kWide) - 1) & 1))) {
-          give_up();
-          ok = false;
-          break;
-        }
-        const uint8_t* src = ring + slot * S_::kStage8 + tv * S_::kTile8;
-        uint8_t* dst = wide + b * S_::kStage16 + tv * S_::kTile16;
-        const bool inner = u.keys.inner(t);
-#pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-          const int e = lane + 32 * i;
-          const int row = 32 * half + (e >> 3), c = e & 7;
-          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-          const int p = u.keys.chunk(kStepChunks * t + (row >> 4)) * kChunkKeys + (row & 15);
-          if (tv == 0 || inner || u.keys.any_sees(p)) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + sw(row, c));
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = e4m3x2_f16x2(in[j] & 0xffffu);
-              y[2 * j + 1] = e4m3x2_f16x2(in[j] >> 16);
-            }
-            if constexpr (BS) {
-              const uint32_t rb = s_ratio[g % kScaleRing][tv * kStepChunks + (row >> 4)];
-              const __half2 ratio = *reinterpret_cast<const __half2*>(&rb);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[j]), ratio);
-                y[j] = *reinterpret_cast<const uint32_t*>(&z);
-              }
-            }
-            lo = make_uint4(y[0], y[1], y[2], y[3]);
-            hi = make_uint4(y[4], y[5], y[6], y[7]);
-          }
-          // head_dim 16 c .. 16 c + 15: slab c / 4, pieces 2 (c % 4) and the next
-          uint8_t* d = dst + (c >> 2) * kSlab;
-          *reinterpret_cast<uint4*>(d + sw(row, 2 * (c & 3))) = lo;
-          *reinterpret_cast<uint4*>(d + sw(row, 2 * (c & 3) + 1)) = hi;
-        }
-        fence_proxy_async();   // the widened rows, before the tensor core reads them
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&conv_full[b]));
-          mbar_arrive(smem_u32(&empty[slot]));
-        }
-      }
-    }
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ softmax
-    // every branch around a warp-wide TMEM access is taken by the whole warp
-    const int X = warp >> 2, r = tid & 127, rp = tid;   // tile, TMEM lane, row of the pair
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tX = tmem + 256 * X + lane_off, tO = tX + 128;
-    uint8_t* qx = q_s + X * S_::kQTile;
-    constexpr int kPieces = D / 8;            // 16-byte pieces of a row
-    constexpr int kPer = kRows / (kRows / kPieces);
-    // The tile's query rows, a 16-byte piece a thread: a warp reads whole rows
-    auto load_q = [&](const Unit& u) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int row = r / kPieces + i * (kRows / kPieces), c = r % kPieces;
-        uint8_t* d = qx + (c >> 3) * kQSlab + sw(row, c & 7);
-        const int rr = kRows * X + row;
-        if (rr < u.in_pair)
-          cp_async16(smem_u32(d), static_cast<const typename Q::raw*>(a.q) + u.row_at(rr, a, D) + 8 * c);
+  } else if (warp >= kHelpWarp) {
+    // -------------------------------------------------------------- helpers
+    // Four warps load the queries of each unit, write its output, and, for
+    // E4M3 caches, widen its K (two warps) and V (the other two).  A unit's
+    // queries follow as soon as the last S of the unit before is done; its
+    // first two steps are widened before that unit's output is waited for.
+    const int hw = warp - kHelpWarp, ht = tid - 32 * kHelpWarp;
+    constexpr int kPieces = D / 8;                 // 16-byte pieces of a query row
+    constexpr int kRowStep = kRows / kPieces;      // rows the 128 threads cover at a time
+    const int qc = ht % kPieces, qr = ht / kPieces;
+    const int di = kRowStep / G, dj = kRowStep - di * G;
+    auto load_q = [&](const Unit& u, int X) {
+      uint8_t* qx = q_s + X * S_::kQTile + (qc >> 3) * kQSlab;
+      int i = (u.row0 + kRows * X + qr) / G, j = u.row0 + kRows * X + qr - i * G;
+#pragma unroll 8
+      for (int row = qr; row < kRows; row += kRowStep) {
+        uint8_t* d = qx + sw(row, qc & 7);
+        if (kRows * X + row < u.in_pair)
+          cp_async16(smem_u32(d), static_cast<const typename Q::raw*>(a.q) + u.at(i, j, a, D) + 8 * qc);
         else
           *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);   // past the chunk's end
+        i += di;
+        j += dj;
+        if (j >= G) {
+          j -= G;
+          ++i;
+        }
       }
     };
-    auto announce_q = [&]() {
-      cp_async_wait();
+    auto announce_q = [&](int X) {
       if constexpr (kFp8 && kOutBf) {   // the MMA is f16: the thread's own pieces
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int row = r / kPieces + i * (kRows / kPieces), c = r % kPieces;
-          uint4* d = reinterpret_cast<uint4*>(qx + (c >> 3) * kQSlab + sw(row, c & 7));
+        uint8_t* qx = q_s + X * S_::kQTile + (qc >> 3) * kQSlab;
+#pragma unroll 4
+        for (int row = qr; row < kRows; row += kRowStep) {
+          uint4* d = reinterpret_cast<uint4*>(qx + sw(row, qc & 7));
           uint4 v = *d;
           float f[8];
           LoadF32<Q, 8>::run(&v, f);
@@ -626,26 +610,167 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
       fence_proxy_async();
       mbar_arrive(smem_u32(&q_full[X]));
     };
-    int g = 0, c = 0;   // stream steps and this tile's steps so far
-    bool ok = true;
-    Work w;
-    bool more = next_work(0, w);
-    if (more) {
-      const Unit u(w, a);
-      if (X == 0 || u.nt[1] > 0) {
-        load_q(u);
-        announce_q();
+    int g = 0, c[2] = {0, 0}, units[2] = {0, 0}, loads[2] = {0, 0};
+    auto queries = [&](const Unit& u) -> bool {
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        if (X == 1 && u.nt[1] == 0) continue;
+        // the tile's last S of the unit before is done
+        if (loads[X] > 0 && !wait(&q_free[X], (loads[X] - 1) & 1)) return false;
+        load_q(u, X);
+        ++loads[X];
       }
-    }
+      cp_async_wait();
+      announce_q(0);
+      if (u.nt[1] > 0) announce_q(1);
+      return true;
+    };
+    // Steps [t0, t1) of a unit, widened; each warp half of the 64 rows of K or
+    // V, a 16-byte piece (16 elements) a lane at a time.
+    auto widen = [&](const Unit& u, int t0, int t1) -> bool {
+      const int tv = hw >> 1, half = hw & 1;
+      uint64_t* done = tv ? v_full : k_full;
+      uint64_t* freed = tv ? v_free : k_free;
+      const int bufs = tv ? kWideV : kWideK;
+      uint8_t* buf0 = tv ? v16 : k16;
+      for (int t = t0; t < t1; ++t) {
+        const int gt = g + t, slot = gt % kRing, b = gt % bufs;
+        if (!wait(&full[slot], (gt / kRing) & 1)) return false;
+        if (gt >= bufs && !wait(&freed[b], ((gt / bufs) - 1) & 1)) return false;
+        const uint8_t* src = ring + slot * S_::kStage + tv * S_::kTile;
+        uint8_t* dst = buf0 + b * S_::kTile16;
+        const bool all = tv == 0 || u.keys.inner(t);
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          const int e = lane + 32 * i;
+          const int row = 32 * half + (e >> 3), cc = e & 7;
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (all || u.keys.any_sees(u.keys.chunk(kStepChunks * t + (row >> 4)) * kChunkKeys + (row & 15))) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + sw(row, cc));
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[2 * j] = e4m3x2_f16x2(in[j] & 0xffffu);
+              y[2 * j + 1] = e4m3x2_f16x2(in[j] >> 16);
+            }
+            if constexpr (BS) {
+              const __half2 ratio = __half2half2(s_ratio[gt % kScaleRing][tv * kStepChunks + (row >> 4)]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[j]), ratio);
+                y[j] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+            }
+            lo = make_uint4(y[0], y[1], y[2], y[3]);
+            hi = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          // head_dim 16 cc .. 16 cc + 15: slab cc / 4, pieces 2 (cc % 4) and the next
+          uint8_t* d = dst + (cc >> 2) * kSlab;
+          *reinterpret_cast<uint4*>(d + sw(row, 2 * (cc & 3))) = lo;
+          *reinterpret_cast<uint4*>(d + sw(row, 2 * (cc & 3) + 1)) = hi;
+        }
+        fence_proxy_async();   // the widened rows, before the tensor core reads them
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&done[b]));
+          mbar_arrive(smem_u32(&empty[slot]));
+        }
+      }
+      return true;
+    };
+    // O / l of unit u (the CTA's k-th) into its rows.  Lane pairs swap 16-byte
+    // pieces, so that two lanes store 32 bytes of one row.
+    auto output = [&](const Unit& u, int k) -> bool {
+#pragma unroll 1
+      for (int X = 0; X < 2; ++X) {
+        const int nt = X ? u.nt[1] : u.nt[0];
+        if (nt == 0) continue;
+        const int cl = c[X] + nt - 1;
+        if (!wait(&l_full[X], units[X] & 1) || !wait(&o_done[2 * X + (cl & 1)], (cl >> 1) & 1)) return false;
+        tc_fence_after();
+        const int r = 32 * hw + lane;   // TMEM lane, row of the tile
+        const bool bad = *reinterpret_cast<volatile int*>(&s_work[k & 1].bad) != 0;
+        const float inv = s_inv[X][r];
+        // rows of the pair of lanes: r & ~1 and the next
+        typename Q::raw* dst[2];
+        bool in[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = kRows * X + (r & ~1) + e;
+          in[e] = rr < u.in_pair;
+          const int i = (u.row0 + min(rr, u.in_pair - 1)) / G, j = u.row0 + min(rr, u.in_pair - 1) - i * G;
+          dst[e] = static_cast<typename Q::raw*>(a.out) + u.at(i, j, a, D) + 8 * (lane & 1);
+        }
+        const uint32_t tO = tmem + 256 * X + 128 + (static_cast<uint32_t>(32 * hw) << 16);
+#pragma unroll 1
+        for (int e0 = 0; e0 < D; e0 += 32) {
+          float o[32];
+          tmem_ld32(tO + e0, o);
+          if (e0 + 32 == D) {   // O is in registers: the next unit's first P V may replace it
+            tc_fence_before();
+            mbar_arrive(smem_u32(&o_free[X]));
+          }
+          uint32_t ow[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            ow[e] = pack2<kOutBf>(bad ? CUDART_NAN_F : o[2 * e] * inv, bad ? CUDART_NAN_F : o[2 * e + 1] * inv);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {   // pieces 2 p and 2 p + 1 of these 32 columns
+            uint32_t even[4], odd[4];     // what goes to the pair's first and second row
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t mine0 = ow[8 * p + e], mine1 = ow[8 * p + 4 + e];
+              const uint32_t got = __shfl_xor_sync(FULL, (lane & 1) ? mine0 : mine1, 1);
+              even[e] = (lane & 1) ? got : mine0;
+              odd[e] = (lane & 1) ? mine1 : got;
+            }
+            if (in[0]) *reinterpret_cast<uint4*>(dst[0] + e0 + 16 * p) = make_uint4(even[0], even[1], even[2], even[3]);
+            if (in[1]) *reinterpret_cast<uint4*>(dst[1] + e0 + 16 * p) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
+          }
+        }
+        if (r == 0 && bad && a.status != nullptr) atomicOr(a.status, s_work[k & 1].bad);
+        c[X] += nt;
+        ++units[X];
+      }
+      if (ht == 0) s_finished = k + 1;
+      return true;
+    };
+    Work w;
+    bool more = next_work(0, w), ok = true;
     for (int k = 0; more && ok; ++k) {
       const Unit u(w, a);
+      if (k == 0) ok = queries(u) && (!kFp8 || widen(u, 0, min(2, u.steps)));
+      if (ok && kFp8) ok = widen(u, min(2, u.steps), u.steps);
+      g += u.steps;
+      if (!ok) break;
+      more = next_work(k + 1, w);
+      if (more) {
+        const Unit v(w, a);
+        ok = queries(v) && (!kFp8 || widen(v, 0, min(2, v.steps)));
+      }
+      if (ok) ok = output(u, k);
+      release_work(k);
+    }
+    if (!ok) give_up();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    // every branch around a warp-wide TMEM access is taken by the whole warp
+    const int X = warp >> 2, r = tid & 127, rp = tid;   // tile, TMEM lane, row of the pair
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tX = tmem + 256 * X + lane_off, tO = tX + 128;
+    int g = 0, c = 0, units = 0;   // stream steps, this tile's steps and units so far
+    bool ok = true;
+    Work w;
+    for (int k = 0; ok && next_work(k, w); ++k) {
+      const Unit u(w, a);
+      release_work(k);
       const int ntx = X ? u.nt[1] : u.nt[0];
       const HeadScales hs = head_scales(a.head_scales, a.num_kv_heads, u.kvh, a.softmax_scale, a.qk_scale,
                                         a.v_scale, 1.f, 1.f);
       const int pos = u.pos_of(min(rp, u.in_pair - 1), G);
       const int w0 = a.window > 0 ? pos - a.window + 1 : 0;
       float m_ref = -CUDART_INF_F, l = 0.f;
-      bool q_next = false;
       for (int t = 0; t < ntx; ++t) {
         const int b = (c + t) & 1, i = 2 * X + b;
         if (!wait(&s_full[i], ((c + t) >> 1) & 1)) {
@@ -665,22 +790,10 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
             sv[32 + e] = __uint_as_float(h1[e]);
           }
         }
-        if (t == ntx - 1) {
-          // the tile's last S is there, so its queries are done with: the
-          // next unit's may take their place
-          more = next_work(k + 1, w);
-          if (more) {
-            const Unit v(w, a);
-            if (X == 0 || v.nt[1] > 0) {
-              load_q(v);
-              q_next = true;
-            }
-          }
-        }
         float qe = hs.qk, lv = 0.f, inv_v = 1.f;
         if constexpr (BS) {
-          // passed already; it orders the producer's scales before this read
-          wait(&conv_full[(g + t) % kWide], ((g + t) / kWide) & 1);
+          // orders the producer's scales before this read
+          wait(&v_full[(g + t) % kWideV], ((g + t) / kWideV) & 1);
           qe *= s_ref[(g + t) % kScaleRing][0];
           const uint32_t vb = __float_as_uint(s_ref[(g + t) % kScaleRing][1]);   // a power of two
           lv = static_cast<float>(static_cast<int>(vb >> 23) - 127);
@@ -705,13 +818,16 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
             if (sv[e] != -CUDART_INF_F) sv[e] *= qe;
           qe = 1.f;
         }
-        float mx8[8];
+        float mx4[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx8[j] = sv[j];
+        for (int j = 0; j < 4; ++j) mx4[j] = sv[j];
 #pragma unroll
-        for (int e = 8; e < 64; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], sv[e]);
-        const float mx = fmaf(qe, fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                        fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))), lv);
+        for (int e = 4; e < 60; e += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx4[j] = max3(mx4[j], sv[e + j], sv[e + 4 + j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx4[j] = fmaxf(mx4[j], sv[60 + j]);
+        const float mx = fmaf(qe, fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]), lv);
         const bool move = mx > m_ref + kRescaleLog2;
         const bool scale = move && t > 0 && m_ref != -CUDART_INF_F;   // O holds earlier steps
         if (__any_sync(FULL, scale)) {
@@ -735,28 +851,29 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
         if (move) m_ref = mx;
         // a row that has seen nothing yet keeps every weight 0
         const float off = lv - (m_ref == -CUDART_INF_F ? 0.f : m_ref);
-        float sum8[8];
+        const float2 qe2 = make_float2(qe, qe), off2 = make_float2(off, off);
+        float2 sum2[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum8[j] = 0.f;
+        for (int j = 0; j < 4; ++j) sum2[j] = make_float2(0.f, 0.f);
         uint32_t pw[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float e0 = ex2(fmaf(sv[2 * e], qe, off));
-          const float e1 = ex2(fmaf(sv[2 * e + 1], qe, off));
-          sum8[(2 * e) & 7] += e0;
-          sum8[(2 * e + 1) & 7] += e1;
-          pw[e] = pack2<kBf>(e0, e1);
+          float2 x = fma2(make_float2(sv[2 * e], sv[2 * e + 1]), qe2, off2);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          sum2[e & 3] = add2(sum2[e & 3], x);
+          pw[e] = pack2<kBf>(x.x, x.y);
         }
         tmem_st32u(tX + 64 * b, pw);
-        l = fmaf(((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7])),
-                 inv_v, l);
-        // V rows that nobody sees (16-bit caches; the converters leave zeros);
+        const float2 sum = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
+        l = fmaf(sum.x + sum.y, inv_v, l);
+        // V rows that nobody sees (16-bit caches; the helpers leave zeros);
         // both tiles' threads write them, each before its own P V
         if constexpr (!kFp8) {
           if (!u.keys.inner(t) && r < kKeys) {
             const int p = u.keys.chunk(kStepChunks * t + (r >> 4)) * kChunkKeys + (r & 15);
             if (!u.keys.any_sees(p)) {
-              uint8_t* vt = ring + ((g + t) % S_::kRing) * S_::kStage16 + S_::kTile16 + r * 128;
+              uint8_t* vt = ring + ((g + t) % kRing) * S_::kStage + S_::kTile + r * 128;
 #pragma unroll
               for (int e = 0; e < 8 * S_::kSlabs; ++e)
                 *reinterpret_cast<uint4*>(vt + (e >> 3) * kSlab + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -767,58 +884,19 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[i]));
       }
-      if (!ok) {
-        give_up();
-        break;
-      }
-      if (ntx == 0) {   // tile B has no rows in this unit
-        more = next_work(k + 1, w);
-        if (more) {
-          const Unit v(w, a);
-          if (v.nt[1] > 0) {
-            load_q(v);
-            q_next = true;
-          }
+      if (ok && ntx > 0) {
+        // the row's factor for the helpers, who are done with the unit before
+        ok = units == 0 || wait(&o_free[X], (units - 1) & 1);
+        if (ok) {
+          s_inv[X][r] = (l > 0.f || l != l) ? hs.v / l : 0.f;
+          mbar_arrive(smem_u32(&l_full[X]));
         }
+        ++units;
       }
-      if (q_next) announce_q();
-      // epilogue: O / l, after the tile's last P V
-      if (ntx > 0) {
-        const int cl = c + ntx - 1;
-        if (!wait(&o_done[2 * X + (cl & 1)], (cl >> 1) & 1)) {
-          give_up();
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool bad = *reinterpret_cast<volatile int*>(&s_work[k & 1].bad) != 0;
-        const float inv = bad ? CUDART_NAN_F : (l > 0.f || l != l) ? hs.v / l : 0.f;
-        typename Q::raw* dst = static_cast<typename Q::raw*>(a.out) + u.row_at(min(rp, u.in_pair - 1), a, D);
-#pragma unroll 1
-        for (int e0 = 0; e0 < D; e0 += 32) {
-          float o[32];
-          tmem_ld32(tO + e0, o);
-          if (e0 + 32 == D) {   // O is in registers: the next unit's first P V may replace it
-            tc_fence_before();
-            mbar_arrive(smem_u32(&o_free[X]));
-          }
-          if (rp < u.in_pair) {
-            uint32_t ow[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              ow[e] = pack2<kOutBf>(bad ? CUDART_NAN_F : o[2 * e] * inv, bad ? CUDART_NAN_F : o[2 * e + 1] * inv);
-            uint4* d4 = reinterpret_cast<uint4*>(dst + e0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d4[e] = make_uint4(ow[4 * e], ow[4 * e + 1], ow[4 * e + 2], ow[4 * e + 3]);
-          }
-        }
-        if (r == 0 && bad && a.status != nullptr) atomicOr(a.status, s_work[k & 1].bad);
-      }
-      if (rp == 0) s_finished = k + 1;
-      release_work(k);
       g += u.steps;
       c += ntx;
     }
+    if (!ok) give_up();
   }
 
   // every MMA done and every copy landed before TMEM and shared memory go
@@ -827,8 +905,8 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
     mbar_wait(smem_u32(&fin), 0, kDrainNs);
     if (s_timeout) {
       const int issued = s_issued;
-      for (int t = max(0, issued - S_::kRing); t < issued; ++t)
-        mbar_wait(smem_u32(&full[t % S_::kRing]), (t / S_::kRing) & 1, kDrainNs);
+      for (int t = max(0, issued - kRing); t < issued; ++t)
+        mbar_wait(smem_u32(&full[t % kRing]), (t / kRing) & 1, kDrainNs);
       if (a.status != nullptr) atomicOr(a.status, kTimeout);
     }
   }
@@ -842,7 +920,7 @@ __global__ void __launch_bounds__(Shape<KV, D>::kThreads, 1)
       const Work w = s_work[k & 1];
       if (w.s < 0 || k + 2 < s_claimed) continue;
       const int r0 = w.pair * kUnitRows, rows = min(w.n * G - r0, kUnitRows);
-      for (int i = tid; i < rows * D; i += S_::kThreads) {
+      for (int i = tid; i < rows * D; i += kThreadsW) {
         const int r = r0 + i / D;
         store_elem<Q>(a.out, ((static_cast<int64_t>(w.q0) + r / G) * a.num_q_heads + w.kvh * G + r % G) * D + i % D,
                       CUDART_NAN_F);
@@ -859,7 +937,7 @@ template <typename KV, typename Q, int D, bool BS>
 pkv_status launch(Args a, const CUtensorMap& kmap, const CUtensorMap& vmap, int32_t max_query_len,
                   cudaStream_t st) {
   using S_ = Shape<KV, D>;
-  static_assert(S_::kSmem <= 227 * 1024 - 1024, "ring, queries and the static part fit one SM");
+  static_assert(S_::kSmem <= 227 * 1024 - 2000, "ring, queries and the static part fit one SM");
   auto kernel = prefill_window_kernel<KV, Q, D, BS>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -880,7 +958,7 @@ pkv_status launch(Args a, const CUtensorMap& kmap, const CUtensorMap& vmap, int3
   a.max_q_tiles = max_query_len;   // the longest chunk the caller allows
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units));
-  cfg.blockDim = dim3(S_::kThreads);
+  cfg.blockDim = dim3(kThreadsW);
   cfg.dynamicSmemBytes = S_::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -103,35 +103,60 @@ struct Shape {
 
 using Args = WindowPrefillArgs;
 
-// A claimed unit as the scheduler announces it.
+// 256 rows of one KV head of one chunk, as the scheduler announces them: tile X
+// is rows [128 X, 128 X + 128).
 struct Work {
-  int s, kvh, q0, n, ctx, pair;   // s < 0: no more work
-  int bad;                        // PKV_DEVICE_* bits met while it ran
-};
-
-// 256 rows of one KV head of one chunk, tile X = rows [128 X, 128 X + 128).
-struct Unit {
-  int s, kvh, q0, row0, in_pair, first;
+  int s, kvh, q0, row0, in_pair;   // s < 0: no more work; row0: the unit's first chunk row
+  int pos0, rem0;                  // that row is head rem0 of position pos0
+  int n;                           // of the chunk
   Keys keys;
-  int nt[2], steps;   // 64-key steps of each tile, and of the K/V stream
-  __device__ __forceinline__ Unit(const Work& w, const Args& a) {
-    s = w.s;
-    kvh = w.kvh;
-    q0 = w.q0;
-    row0 = w.pair * kUnitRows;
-    in_pair = min(w.n * a.group - row0, kUnitRows);
-    first = w.ctx - w.n;
-    keys.set(pos_of(0, a.group), pos_of(in_pair - 1, a.group), a.window, a.sinks);
-    const int endA = pos_of(min(in_pair, kRows) - 1, a.group) / kChunkKeys + 1;
+  int nt[2], steps;                // 64-key steps of each tile, and of the K/V stream
+  int bad;                         // PKV_DEVICE_* bits met while it ran
+  __device__ __forceinline__ void set(int seq, int kv_head, int q_first, int len, int ctx, int pair, const Args& a) {
+    const int G = a.group;
+    s = seq;
+    kvh = kv_head;
+    q0 = q_first;
+    n = len;
+    row0 = pair * kUnitRows;
+    in_pair = min(len * G - row0, kUnitRows);
+    const int first = ctx - len;
+    pos0 = first + row0 / G;
+    rem0 = row0 % G;
+    keys.set(pos0, first + (row0 + in_pair - 1) / G, a.window, a.sinks);
+    const int endA = (first + (row0 + min(in_pair, kRows) - 1) / G) / kChunkKeys + 1;
     nt[0] = max((keys.ns + max(endA - keys.wb, 0) + kStepChunks - 1) / kStepChunks, 1);
     steps = (keys.n + kStepChunks - 1) / kStepChunks;
     nt[1] = in_pair > kRows ? steps : 0;
     steps = max(nt[0], nt[1]);
+    bad = 0;
   }
-  __device__ __forceinline__ int pos_of(int r, int G) const { return first + (row0 + r) / G; }
-  // element offset of head j of chunk position i in q and out
-  __device__ __forceinline__ int64_t at(int i, int j, const Args& a, int D) const {
-    return ((static_cast<int64_t>(q0) + i) * a.num_q_heads + kvh * a.group + j) * D;
+  // position and head of row r (< 256) of the unit; inv_g = 1 / G.  rem0 + r is
+  // small, so that the product with half a row added falls on the right side.
+  __device__ __forceinline__ void place(int r, int G, float inv_g, int* pos, int* head) const {
+    const int i = static_cast<int>((static_cast<float>(rem0 + r) + 0.5f) * inv_g);
+    *pos = pos0 + i;
+    *head = rem0 + r - i * G;
+  }
+  // element offset of head j at position pos in q and out
+  __device__ __forceinline__ int64_t at(int pos, int j, const Args& a, int D) const {
+    const int64_t row = static_cast<int64_t>(q0) + (pos - pos0) + row0 / a.group;
+    return (row * a.num_q_heads + kvh * a.group + j) * D;
+  }
+};
+
+// A place in a ring of N buffers and the parity of its use.
+template <int N>
+struct RingPos {
+  int slot = 0;
+  uint32_t par = 0;
+  bool used = false;   // the buffer has been used before
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      par ^= 1;
+      used = true;
+    }
   }
 };
 
@@ -253,7 +278,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   constexpr int kReaders = 15;   // warps that read a unit's description: all but the scheduler
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.group, T = a.block_size;
+  const int G = a.group, HQ = a.num_q_heads, T = a.block_size;
+  const float inv_g = 1.f / static_cast<float>(G);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -269,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
   __shared__ ulonglong2 s_answer;
   __shared__ Work s_work[2];
   __shared__ __half s_ratio[BS ? kScaleRing : 1][2 * kStepChunks];   // scale / R: K, then V chunks
-  __shared__ float s_ref[BS ? kScaleRing : 1][2];                      // R of K and V
+  __shared__ __align__(8) float s_ref[BS ? kScaleRing : 1][2];                      // R of K and V
   __shared__ float s_inv[2][kRows];                                    // 1 / l of a finished row
   __shared__ uint32_t tmem_slot;
   __shared__ int s_timeout, s_issued, s_finished, s_claimed;
@@ -351,7 +377,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         give_up();
         break;
       }
-      Work w{-1, 0, 0, 0, 0, 0, 0};
+      Work w;
+      w.s = -1;
       while (true) {   // until a unit with rows, or the end
         if (x < 0) {   // ask for one more block
           if (lane == 0) {
@@ -370,7 +397,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           if (x < 0) break;
         }
         const int slot = x / a.num_kv_heads;
-        w.kvh = x - slot * a.num_kv_heads;
+        const int kvh = x - slot * a.num_kv_heads;
         x = -1;
         auto slot0 = [&](int s) { return static_cast<int>(static_cast<int64_t>(a.query_start[s]) * G / kUnitRows) + s; };
         int lo = 0, hi = a.num_seqs;   // the last sequence whose slots start at or before `slot`
@@ -388,22 +415,19 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         if (at < 0 || q0 < 0 || n <= 0 || n > a.total_q - q0) continue;   // no rows this call may write
         const int pairs = static_cast<int>((static_cast<int64_t>(n) * G + kUnitRows - 1) / kUnitRows);
         if (at >= pairs) continue;
-        w.q0 = q0;
-        w.n = n;
-        w.ctx = ctx;
-        w.pair = pairs - 1 - at;
+        const int pair = pairs - 1 - at;
         if (ctx < 0 || ctx > a.max_blocks * T || n > ctx || n > a.max_q_tiles) {
-          // invalid lengths: the unit's rows become NaN (w.s stays -1)
+          // invalid lengths: the unit's rows become NaN
           if (lane == 0 && a.status != nullptr) atomicOr(a.status, kBadLength);
-          const int r0 = w.pair * kUnitRows, rows = min(n * G - r0, kUnitRows);
+          const int r0 = pair * kUnitRows, rows = min(n * G - r0, kUnitRows);
           for (int i = lane; i < rows * D; i += 32) {
             const int r = r0 + i / D;
-            store_elem<Q>(a.out, ((static_cast<int64_t>(q0) + r / G) * a.num_q_heads + w.kvh * G + r % G) * D + i % D,
+            store_elem<Q>(a.out, ((static_cast<int64_t>(q0) + r / G) * a.num_q_heads + kvh * G + r % G) * D + i % D,
                           CUDART_NAN_F);
           }
           continue;
         }
-        w.s = lo;
+        w.set(lo, kvh, q0, n, ctx, pair, a);
         break;
       }
       __syncwarp();
@@ -422,10 +446,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     constexpr int kBoxes = kStepChunks * kBoxSlabs * 2;
     const int bv = lane & 1, bsl = (lane >> 1) % kBoxSlabs, bc = (lane >> 1) / kBoxSlabs;
     int g = 0;   // steps of the K/V stream so far
+    RingPos<kRing> at;
     bool ok = true;
     Work w;
     for (int k = 0; ok && next_work(k, w); ++k) {
-      const Unit u(w, a);
+      const Work& u = w;
       const int32_t* trow = a.tables + static_cast<size_t>(u.s) * a.max_blocks;
       // lane l of batch b: the pool row (-1: none) and the scales of chunk 32 b + l
       auto fetch = [&](int b, int& row, float2& sc) {
@@ -450,14 +475,14 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       float2 sc_cur, sc_nxt;
       fetch(0, row_cur, sc_cur);
       fetch(1, row_nxt, sc_nxt);
-      for (int t = 0; t < u.steps; ++t, ++g) {
+      for (int t = 0; t < u.steps; ++t, ++g, at.next()) {
         if ((t & 7) == 0 && t > 0) {   // 32 chunks are 8 steps
           row_cur = row_nxt;
           sc_cur = sc_nxt;
           fetch(t / 8 + 1, row_nxt, sc_nxt);
         }
-        const int slot = g % kRing;
-        if (g >= kRing && !wait(&empty[slot], ((g / kRing) - 1) & 1)) {
+        const int slot = at.slot;
+        if (at.used && !wait(&empty[slot], at.par ^ 1)) {
           give_up();
           ok = false;
           break;
@@ -500,69 +525,68 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     const uint64_t q_desc = sw128_desc(smem_u32(q_s + X * S_::kQTile), 16, 1024);
     const uint64_t k_desc = sw128_desc(smem_u32(k16), 16, 1024);
     const uint64_t v_desc = sw128_desc(smem_u32(v16), kSlab, 1024);
-    int g = 0, c = 0, units = 0;   // stream steps, this tile's steps and units so far
+    RingPos<kBufK> kp;   // of the next Q K^T
+    RingPos<kBufV> vp;   // of the next P V
+    RingPos<2> sq, sp;   // S / P buffers of the next Q K^T and the next P V
+    int units = 0;       // of this tile so far
     bool ok = true;
     Work w;
     for (int k = 0; ok && next_work(k, w); ++k) {
-      const Unit u(w, a);
+      const int nt = X ? w.nt[1] : w.nt[0], steps = w.steps;
       release_work(k);
-      const int nt = X ? u.nt[1] : u.nt[0];
-      auto qk = [&](int t) -> bool {
-        const int slot = (g + t) % kBufK, i = 2 * X + ((c + t) & 1), use = (c + t) >> 1;
-        if (!wait(kFp8 ? &k_full[slot] : &full[slot], ((g + t) / kBufK) & 1)) return false;
+      auto qk = [&](bool last) -> bool {
+        const int i = 2 * X + sq.slot;
+        if (!wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par)) return false;
         // the buffer's step before: its P has been read by P V
-        if (use >= 1 && !wait(&o_done[i], (use - 1) & 1)) return false;
+        if (sq.used && !wait(&o_done[i], sq.par ^ 1)) return false;
         tc_fence_after();
-        const uint64_t kd = k_desc + ((slot * S_::kStrideK) >> 4);
-        const uint32_t d_tmem = tm + 64 * ((c + t) & 1);
+        const uint64_t kd = k_desc + static_cast<uint32_t>(kp.slot * (S_::kStrideK >> 4));
+        const uint32_t d_tmem = tm + 64 * sq.slot;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           mma_ss(leader, d_tmem, q_desc + (((ks >> 2) * kQSlab + 32 * (ks & 3)) >> 4),
                  kd + (((ks >> 2) * kSlab + 32 * (ks & 3)) >> 4), kIdQK, ks > 0 ? 1u : 0u);
         commit(leader, smem_u32(&s_full[i]));
-        if (kFp8) commit(leader, smem_u32(&k_free[slot]));
-        if (t == nt - 1) commit(leader, smem_u32(&q_free[X]));
+        if (kFp8) commit(leader, smem_u32(&k_free[kp.slot]));
+        if (last) commit(leader, smem_u32(&q_free[X]));
+        kp.next();
+        sq.next();
         return true;
       };
-      auto pv = [&](int t) -> bool {
-        const int slot = (g + t) % kBufV, i = 2 * X + ((c + t) & 1);
-        if (kFp8 && !wait(&v_full[slot], ((g + t) / kBufV) & 1)) return false;
-        if (!wait(&p_full[i], ((c + t) >> 1) & 1)) return false;
+      auto pv = [&](bool first) -> bool {
+        const int i = 2 * X + sp.slot;
+        if (kFp8 && !wait(&v_full[vp.slot], vp.par)) return false;
         // O of the unit before has been read
-        if (t == 0 && units > 0 && !wait(&o_free[X], (units - 1) & 1)) return false;
+        if (first && units > 0 && !wait(&o_free[X], (units - 1) & 1)) return false;
+        if (!wait(&p_full[i], sp.par)) return false;
         tc_fence_after();
-        const uint64_t vd = v_desc + ((slot * S_::kStrideV) >> 4);
-        const uint32_t p_tmem = tm + 64 * ((c + t) & 1);
+        const uint64_t vd = v_desc + static_cast<uint32_t>(vp.slot * (S_::kStrideV >> 4));
+        const uint32_t p_tmem = tm + 64 * sp.slot;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(leader, tm + 128, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (t > 0 || kk > 0) ? 1u : 0u);
+          mma_ts(leader, tm + 128, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
         commit(leader, smem_u32(&o_done[i]));
-        commit(leader, smem_u32(kFp8 ? &v_free[slot] : &empty[slot]));
+        commit(leader, smem_u32(kFp8 ? &v_free[vp.slot] : &empty[vp.slot]));
+        vp.next();
+        sp.next();
         return true;
       };
       if (nt > 0) {
-        ok = wait(&q_full[X], units & 1) && qk(0) && (nt < 2 || qk(1));
-        for (int t = 0; t < nt && ok; ++t) ok = pv(t) && (t + 2 >= nt || qk(t + 2));
+        ok = wait(&q_full[X], units & 1) && qk(nt == 1) && (nt < 2 || qk(nt == 2));
+        for (int t = 0; t < nt && ok; ++t) ok = pv(t == 0) && (t + 2 >= nt || qk(t + 3 == nt));
         ++units;
       }
       // the stream's steps that only the other tile reads
-      for (int t = nt; t < u.steps && ok; ++t) {
-        if constexpr (kFp8) {
-          const int sk = (g + t) % kBufK, sv = (g + t) % kBufV;
-          ok = wait(&k_full[sk], ((g + t) / kBufK) & 1) && wait(&v_full[sv], ((g + t) / kBufV) & 1);
-          if (ok && lane == 0) {
-            mbar_arrive(smem_u32(&k_free[sk]));
-            mbar_arrive(smem_u32(&v_free[sv]));
-          }
-        } else {
-          const int slot = (g + t) % kRing;
-          ok = wait(&full[slot], ((g + t) / kRing) & 1);
-          if (ok && lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+      for (int t = nt; t < steps && ok; ++t) {
+        ok = wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par) && (!kFp8 || wait(&v_full[vp.slot], vp.par));
+        if (ok && lane == 0) {
+          if (kFp8) mbar_arrive(smem_u32(&k_free[kp.slot]));
+          mbar_arrive(smem_u32(kFp8 ? &v_free[vp.slot] : &empty[vp.slot]));
         }
+        kp.next();
+        vp.next();
       }
       if (!ok) give_up();
-      g += u.steps;
-      c += nt;
     }
     commit(leader, smem_u32(&fin));
   } else if (warp >= kHelpWarp) {
@@ -576,21 +600,25 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     constexpr int kRowStep = kRows / kPieces;      // rows the 128 threads cover at a time
     const int qc = ht % kPieces, qr = ht / kPieces;
     const int di = kRowStep / G, dj = kRowStep - di * G;
-    auto load_q = [&](const Unit& u, int X) {
-      uint8_t* qx = q_s + X * S_::kQTile + (qc >> 3) * kQSlab;
-      int i = (u.row0 + kRows * X + qr) / G, j = u.row0 + kRows * X + qr - i * G;
-#pragma unroll 8
+    const int64_t step = (static_cast<int64_t>(di) * HQ + dj) * D, wrap = static_cast<int64_t>(HQ - G) * D;
+    // rows qr, qr + kRowStep, .. of tile X: eight rows on, a piece keeps its
+    // place in the swizzle
+    auto load_q = [&](const Work& u, int X) {
+      uint32_t d = smem_u32(q_s + X * S_::kQTile + (qc >> 3) * kQSlab + sw(qr, qc & 7));
+      int pos, j;
+      u.place(kRows * X + qr, G, inv_g, &pos, &j);
+      const typename Q::raw* src = static_cast<const typename Q::raw*>(a.q) + u.at(pos, j, a, D) + 8 * qc;
+      const int rows = u.in_pair - kRows * X;   // of the tile inside the chunk
+#pragma unroll 4
       for (int row = qr; row < kRows; row += kRowStep) {
-        uint8_t* d = qx + sw(row, qc & 7);
-        if (kRows * X + row < u.in_pair)
-          cp_async16(smem_u32(d), static_cast<const typename Q::raw*>(a.q) + u.at(i, j, a, D) + 8 * qc);
-        else
-          *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);   // past the chunk's end
-        i += di;
+        if (row < rows) cp_async16(d, src);
+        else asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d), "r"(0) : "memory");
+        d += kRowStep * 128;
+        src += step;
         j += dj;
         if (j >= G) {
           j -= G;
-          ++i;
+          src += wrap;
         }
       }
     };
@@ -610,84 +638,116 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       fence_proxy_async();
       mbar_arrive(smem_u32(&q_full[X]));
     };
-    int g = 0, c[2] = {0, 0}, units[2] = {0, 0}, loads[2] = {0, 0};
-    auto queries = [&](const Unit& u) -> bool {
+    int g = 0;   // steps widened so far
+    int units[2] = {0, 0}, loads[2] = {0, 0};
+    int last_buf[2] = {1, 1};   // S / P buffer of the tile's last step so far
+    uint32_t last_par[2] = {1, 1};
+    auto queries = [&](const Work& u) -> bool {
 #pragma unroll
       for (int X = 0; X < 2; ++X) {
         if (X == 1 && u.nt[1] == 0) continue;
         // the tile's last S of the unit before is done
         if (loads[X] > 0 && !wait(&q_free[X], (loads[X] - 1) & 1)) return false;
         load_q(u, X);
+        cp_async_wait();
+        announce_q(X);
         ++loads[X];
       }
-      cp_async_wait();
-      announce_q(0);
-      if (u.nt[1] > 0) announce_q(1);
       return true;
     };
     // Steps [t0, t1) of a unit, widened; each warp half of the 64 rows of K or
-    // V, a 16-byte piece (16 elements) a lane at a time.
-    auto widen = [&](const Unit& u, int t0, int t1) -> bool {
-      const int tv = hw >> 1, half = hw & 1;
+    // V, a 16-byte piece (16 elements) a lane at a time.  Lanes of the upper
+    // head_dim half store their two pieces in the other order: the two halves'
+    // slabs share banks.
+    const int tv = hw >> 1, half = hw & 1;
+    RingPos<kRing> at;
+    int buf = 0;
+    uint32_t buf_par = 0;
+    bool buf_used = false;
+    auto widen = [&](const Work& u, int t0, int t1) -> bool {
       uint64_t* done = tv ? v_full : k_full;
       uint64_t* freed = tv ? v_free : k_free;
       const int bufs = tv ? kWideV : kWideK;
-      uint8_t* buf0 = tv ? v16 : k16;
+      const int rl = lane >> 3, cc = lane & 7;   // row of four, piece of its 8
+      const bool upper = cc >= 4;
       for (int t = t0; t < t1; ++t) {
-        const int gt = g + t, slot = gt % kRing, b = gt % bufs;
-        if (!wait(&full[slot], (gt / kRing) & 1)) return false;
-        if (gt >= bufs && !wait(&freed[b], ((gt / bufs) - 1) & 1)) return false;
-        const uint8_t* src = ring + slot * S_::kStage + tv * S_::kTile;
-        uint8_t* dst = buf0 + b * S_::kTile16;
-        const bool all = tv == 0 || u.keys.inner(t);
-#pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-          const int e = lane + 32 * i;
-          const int row = 32 * half + (e >> 3), cc = e & 7;
-          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-          if (all || u.keys.any_sees(u.keys.chunk(kStepChunks * t + (row >> 4)) * kChunkKeys + (row & 15))) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + sw(row, cc));
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
+        if (!wait(&full[at.slot], at.par)) return false;
+        if (buf_used && !wait(&freed[buf], buf_par ^ 1)) return false;
+        const uint8_t* src = ring + at.slot * S_::kStage + tv * S_::kTile;
+        uint8_t* dst = (tv ? v16 : k16) + buf * S_::kTile16 + (cc >> 2) * kSlab;
+        __half2 ratio[2];
+        if constexpr (BS) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = e4m3x2_f16x2(in[j] & 0xffffu);
-              y[2 * j + 1] = e4m3x2_f16x2(in[j] >> 16);
-            }
-            if constexpr (BS) {
-              const __half2 ratio = __half2half2(s_ratio[gt % kScaleRing][tv * kStepChunks + (row >> 4)]);
+          for (int e = 0; e < 2; ++e)
+            ratio[e] = __half2half2(s_ratio[g % kScaleRing][tv * kStepChunks + 2 * half + e]);
+        }
+        auto piece = [&](int i, const uint4& x) {
+          const int row = 32 * half + 4 * i + rl;
+          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[j]), ratio);
-                y[j] = *reinterpret_cast<const uint32_t*>(&z);
-              }
-            }
-            lo = make_uint4(y[0], y[1], y[2], y[3]);
-            hi = make_uint4(y[4], y[5], y[6], y[7]);
+          for (int j = 0; j < 4; ++j) {
+            y[2 * j] = e4m3x2_f16x2(in[j] & 0xffffu);
+            y[2 * j + 1] = e4m3x2_f16x2(in[j] >> 16);
           }
-          // head_dim 16 cc .. 16 cc + 15: slab cc / 4, pieces 2 (cc % 4) and the next
-          uint8_t* d = dst + (cc >> 2) * kSlab;
-          *reinterpret_cast<uint4*>(d + sw(row, 2 * (cc & 3))) = lo;
-          *reinterpret_cast<uint4*>(d + sw(row, 2 * (cc & 3) + 1)) = hi;
+          if constexpr (BS) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[j]), ratio[i >> 2]);
+              y[j] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          // head_dim 16 cc .. 16 cc + 15: pieces 2 (cc % 4) and the next of slab cc / 4
+          const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+          *reinterpret_cast<uint4*>(dst + sw(row, 2 * (cc & 3) + upper)) = upper ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + sw(row, 2 * (cc & 3) + !upper)) = upper ? lo : hi;
+        };
+        if (tv == 0 || u.keys.inner(t)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x[i] = *reinterpret_cast<const uint4*>(src + sw(32 * half + 16 * h + 4 * i + rl, cc));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) piece(4 * h + i, x[i]);
+          }
+        } else {   // V rows that nobody sees become zeros
+          for (int i = 0; i < 8; ++i) {
+            const int row = 32 * half + 4 * i + rl;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (u.keys.any_sees(u.keys.chunk(kStepChunks * t + (row >> 4)) * kChunkKeys + (row & 15)))
+              x = *reinterpret_cast<const uint4*>(src + sw(row, cc));
+            piece(i, x);
+          }
         }
         fence_proxy_async();   // the widened rows, before the tensor core reads them
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&done[b]));
-          mbar_arrive(smem_u32(&empty[slot]));
+          mbar_arrive(smem_u32(&done[buf]));
+          mbar_arrive(smem_u32(&empty[at.slot]));
+        }
+        at.next();
+        ++g;
+        if (++buf == bufs) {
+          buf = 0;
+          buf_par ^= 1;
+          buf_used = true;
         }
       }
       return true;
     };
     // O / l of unit u (the CTA's k-th) into its rows.  Lane pairs swap 16-byte
     // pieces, so that two lanes store 32 bytes of one row.
-    auto output = [&](const Unit& u, int k) -> bool {
-#pragma unroll 1
+    auto output = [&](const Work& u, int k) -> bool {
+#pragma unroll
       for (int X = 0; X < 2; ++X) {
         const int nt = X ? u.nt[1] : u.nt[0];
         if (nt == 0) continue;
-        const int cl = c[X] + nt - 1;
-        if (!wait(&l_full[X], units[X] & 1) || !wait(&o_done[2 * X + (cl & 1)], (cl >> 1) & 1)) return false;
+        // the buffer and parity of the tile's last step: nt steps on
+        last_par[X] ^= ((last_buf[X] + nt) >> 1) & 1;
+        last_buf[X] = (last_buf[X] + nt) & 1;
+        if (!wait(&l_full[X], units[X] & 1) || !wait(&o_done[2 * X + last_buf[X]], last_par[X])) return false;
         tc_fence_after();
         const int r = 32 * hw + lane;   // TMEM lane, row of the tile
         const bool bad = *reinterpret_cast<volatile int*>(&s_work[k & 1].bad) != 0;
@@ -699,8 +759,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         for (int e = 0; e < 2; ++e) {
           const int rr = kRows * X + (r & ~1) + e;
           in[e] = rr < u.in_pair;
-          const int i = (u.row0 + min(rr, u.in_pair - 1)) / G, j = u.row0 + min(rr, u.in_pair - 1) - i * G;
-          dst[e] = static_cast<typename Q::raw*>(a.out) + u.at(i, j, a, D) + 8 * (lane & 1);
+          int pos, j;
+          u.place(min(rr, u.in_pair - 1), G, inv_g, &pos, &j);
+          dst[e] = static_cast<typename Q::raw*>(a.out) + u.at(pos, j, a, D) + 8 * (lane & 1);
         }
         const uint32_t tO = tmem + 256 * X + 128 + (static_cast<uint32_t>(32 * hw) << 16);
 #pragma unroll 1
@@ -730,27 +791,22 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           }
         }
         if (r == 0 && bad && a.status != nullptr) atomicOr(a.status, s_work[k & 1].bad);
-        c[X] += nt;
         ++units[X];
       }
       if (ht == 0) s_finished = k + 1;
       return true;
     };
-    Work w;
-    bool more = next_work(0, w), ok = true;
+    Work u, v;   // the unit at hand and the next
+    bool more = next_work(0, u), ok = true;
+    if (more) ok = queries(u) && (!kFp8 || widen(u, 0, min(2, u.steps)));
     for (int k = 0; more && ok; ++k) {
-      const Unit u(w, a);
-      if (k == 0) ok = queries(u) && (!kFp8 || widen(u, 0, min(2, u.steps)));
-      if (ok && kFp8) ok = widen(u, min(2, u.steps), u.steps);
-      g += u.steps;
+      if (kFp8) ok = widen(u, min(2, u.steps), u.steps);
       if (!ok) break;
-      more = next_work(k + 1, w);
-      if (more) {
-        const Unit v(w, a);
-        ok = queries(v) && (!kFp8 || widen(v, 0, min(2, v.steps)));
-      }
+      more = next_work(k + 1, v);
+      if (more) ok = queries(v) && (!kFp8 || widen(v, 0, min(2, v.steps)));
       if (ok) ok = output(u, k);
       release_work(k);
+      u = v;
     }
     if (!ok) give_up();
   } else if (warp < 8) {
@@ -759,21 +815,24 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     const int X = warp >> 2, r = tid & 127, rp = tid;   // tile, TMEM lane, row of the pair
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tX = tmem + 256 * X + lane_off, tO = tX + 128;
-    int g = 0, c = 0, units = 0;   // stream steps, this tile's steps and units so far
+    RingPos<2> sp;             // S / P buffer
+    RingPos<kRing> at;         // stage of the stream
+    RingPos<kWideV> av;        // widened V buffer
+    int g = 0, units = 0;      // stream steps and this tile's units so far
     bool ok = true;
-    Work w;
-    for (int k = 0; ok && next_work(k, w); ++k) {
-      const Unit u(w, a);
+    Work u;
+    for (int k = 0; ok && next_work(k, u); ++k) {
       release_work(k);
       const int ntx = X ? u.nt[1] : u.nt[0];
       const HeadScales hs = head_scales(a.head_scales, a.num_kv_heads, u.kvh, a.softmax_scale, a.qk_scale,
                                         a.v_scale, 1.f, 1.f);
-      const int pos = u.pos_of(min(rp, u.in_pair - 1), G);
+      int pos, head;
+      u.place(min(rp, u.in_pair - 1), G, inv_g, &pos, &head);
       const int w0 = a.window > 0 ? pos - a.window + 1 : 0;
       float m_ref = -CUDART_INF_F, l = 0.f;
       for (int t = 0; t < ntx; ++t) {
-        const int b = (c + t) & 1, i = 2 * X + b;
-        if (!wait(&s_full[i], ((c + t) >> 1) & 1)) {
+        const int b = sp.slot, i = 2 * X + b;
+        if (!wait(&s_full[i], sp.par)) {
           ok = false;
           break;
         }
@@ -793,23 +852,25 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         float qe = hs.qk, lv = 0.f, inv_v = 1.f;
         if constexpr (BS) {
           // orders the producer's scales before this read
-          wait(&v_full[(g + t) % kWideV], ((g + t) / kWideV) & 1);
-          qe *= s_ref[(g + t) % kScaleRing][0];
-          const uint32_t vb = __float_as_uint(s_ref[(g + t) % kScaleRing][1]);   // a power of two
+          wait(&v_full[av.slot], av.par);
+          const float2 ref = *reinterpret_cast<const float2*>(s_ref[(g + t) % kScaleRing]);
+          qe *= ref.x;
+          const uint32_t vb = __float_as_uint(ref.y);   // a power of two
           lv = static_cast<float>(static_cast<int>(vb >> 23) - 127);
           inv_v = __uint_as_float((254u << 23) - vb);
         }
         // mask: every key of the step lies in one run of positions unless it
-        // holds sinks' chunks
+        // holds sinks' chunks; elsewhere a bit per key of a chunk
         const int p0 = u.keys.chunk(kStepChunks * t) * kChunkKeys;
         if (!(kStepChunks * t >= u.keys.ns && p0 >= w0 && p0 + kKeys - 1 <= pos)) {
+          auto below = [](int x) { return (1u << min(max(x, 0), kChunkKeys)) - 1u; };   // the first x keys
 #pragma unroll
           for (int ch = 0; ch < kStepChunks; ++ch) {
             const int pc = u.keys.chunk(kStepChunks * t + ch) * kChunkKeys;
-            const int hi = pos - pc, lo = w0 - pc, sk = u.keys.sinks - pc;
+            const uint32_t seen = below(pos - pc + 1) & (~below(w0 - pc) | below(u.keys.sinks - pc));
 #pragma unroll
             for (int e = 0; e < kChunkKeys; ++e)
-              if (e > hi || (e < lo && e >= sk)) sv[16 * ch + e] = -CUDART_INF_F;
+              if (!(seen & (1u << e))) sv[16 * ch + e] = -CUDART_INF_F;
           }
         }
         if (!(qe > 0.f)) {   // the maximum below is taken on the raw products
@@ -831,8 +892,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         const bool move = mx > m_ref + kRescaleLog2;
         const bool scale = move && t > 0 && m_ref != -CUDART_INF_F;   // O holds earlier steps
         if (__any_sync(FULL, scale)) {
-          const int ip = 2 * X + ((c + t - 1) & 1);
-          if (!wait(&o_done[ip], ((c + t - 1) >> 1) & 1)) {
+          if (!wait(&o_done[2 * X + (b ^ 1)], sp.par ^ (b ^ 1))) {   // the step before
             ok = false;
             break;
           }
@@ -873,7 +933,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           if (!u.keys.inner(t) && r < kKeys) {
             const int p = u.keys.chunk(kStepChunks * t + (r >> 4)) * kChunkKeys + (r & 15);
             if (!u.keys.any_sees(p)) {
-              uint8_t* vt = ring + ((g + t) % kRing) * S_::kStage + S_::kTile + r * 128;
+              uint8_t* vt = ring + at.slot * S_::kStage + S_::kTile + r * 128;
 #pragma unroll
               for (int e = 0; e < 8 * S_::kSlabs; ++e)
                 *reinterpret_cast<uint4*>(vt + (e >> 3) * kSlab + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -883,6 +943,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         }
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[i]));
+        sp.next();
+        at.next();
+        if (BS) av.next();
+      }
+      for (int t = ntx; t < u.steps; ++t) {   // the stream's steps of the other tile
+        at.next();
+        if (BS) av.next();
       }
       if (ok && ntx > 0) {
         // the row's factor for the helpers, who are done with the unit before
@@ -894,7 +961,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         ++units;
       }
       g += u.steps;
-      c += ntx;
     }
     if (!ok) give_up();
   }
@@ -919,9 +985,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     for (int k = max(s_finished - 1, 0); k < s_claimed; ++k) {
       const Work w = s_work[k & 1];
       if (w.s < 0 || k + 2 < s_claimed) continue;
-      const int r0 = w.pair * kUnitRows, rows = min(w.n * G - r0, kUnitRows);
-      for (int i = tid; i < rows * D; i += kThreadsW) {
-        const int r = r0 + i / D;
+      for (int i = tid; i < w.in_pair * D; i += kThreadsW) {
+        const int r = w.row0 + i / D;
         store_elem<Q>(a.out, ((static_cast<int64_t>(w.q0) + r / G) * a.num_q_heads + w.kvh * G + r % G) * D + i % D,
                       CUDART_NAN_F);
       }
@@ -953,8 +1018,8 @@ pkv_status launch(Args a, const CUtensorMap& kmap, const CUtensorMap& vmap, int3
   // the blocks that start claim the others one by one
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
   const int64_t units = (rows / kUnitRows + a.num_seqs) * a.num_kv_heads;
-  if (rows > INT32_MAX || units > INT32_MAX)
-    return fail(PKV_ERR_UNSUPPORTED, "windowed prefill: too many query rows in one call");
+  if (rows > INT32_MAX || units > INT32_MAX || a.group > 1024)
+    return fail(PKV_ERR_UNSUPPORTED, "windowed prefill: too many query rows in one call, or query heads per KV head");
   a.max_q_tiles = max_query_len;   // the longest chunk the caller allows
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units));

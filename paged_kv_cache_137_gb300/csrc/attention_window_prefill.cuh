@@ -212,9 +212,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
   return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN if one is
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 
   // a warp-wide bounded wait
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (__all_sync(FULL, mbar_try_wait(smem_u32(bar), parity))) return true;
     return __all_sync(FULL, mbar_wait(smem_u32(bar), parity, kWaitNs));
   };
   // the k-th unit of this CTA: false where there is none (or a wait gave up)
@@ -520,6 +521,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     // ---------------------------------------------------------- MMA issuers
     // one warp a tile: its waits do not hold up the other tile's MMAs
     const int X = warp - kMmaWarp;
+    // no vote: nothing below needs the lanes together (an instruction is its
+    // leader's), and the votes added up in this warp's chain
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(smem_u32(bar), parity, kWaitNs); };
     const uint32_t leader = elect_one();
     const uint32_t tm = __reduce_max_sync(FULL, tmem) + 256 * X;   // uniform for the compiler as well
     const uint64_t q_desc = sw128_desc(smem_u32(q_s + X * S_::kQTile), 16, 1024);
@@ -555,7 +559,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       };
       auto pv = [&](bool first) -> bool {
         const int i = 2 * X + sp.slot;
-        if (kFp8 && !wait(&v_full[vp.slot], vp.par)) return false;
         // O of the unit before has been read
         if (first && units > 0 && !wait(&o_free[X], (units - 1) & 1)) return false;
         if (!wait(&p_full[i], sp.par)) return false;
@@ -829,6 +832,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       int pos, head;
       u.place(min(rp, u.in_pair - 1), G, inv_g, &pos, &head);
       const int w0 = a.window > 0 ? pos - a.window + 1 : 0;
+      // steps [whole0, whole1) lie in one run of keys the row sees entirely
+      const int whole0 = (u.keys.ns + max(max(w0 + kChunkKeys - 1, 0) / kChunkKeys - u.keys.wb, 0) + kStepChunks - 1) / kStepChunks;
+      const int whole1 = ((pos + 1) / kChunkKeys - u.keys.wb + u.keys.ns) / kStepChunks;
       float m_ref = -CUDART_INF_F, l = 0.f;
       for (int t = 0; t < ntx; ++t) {
         const int b = sp.slot, i = 2 * X + b;
@@ -850,19 +856,21 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           }
         }
         float qe = hs.qk, lv = 0.f, inv_v = 1.f;
+        // V widened (before this step's P V, which follows P); it also orders
+        // the producer's scales before their read
+        if (kFp8 && !wait(&v_full[av.slot], av.par)) {
+          ok = false;
+          break;
+        }
         if constexpr (BS) {
-          // orders the producer's scales before this read
-          wait(&v_full[av.slot], av.par);
           const float2 ref = *reinterpret_cast<const float2*>(s_ref[(g + t) % kScaleRing]);
           qe *= ref.x;
           const uint32_t vb = __float_as_uint(ref.y);   // a power of two
           lv = static_cast<float>(static_cast<int>(vb >> 23) - 127);
           inv_v = __uint_as_float((254u << 23) - vb);
         }
-        // mask: every key of the step lies in one run of positions unless it
-        // holds sinks' chunks; elsewhere a bit per key of a chunk
-        const int p0 = u.keys.chunk(kStepChunks * t) * kChunkKeys;
-        if (!(kStepChunks * t >= u.keys.ns && p0 >= w0 && p0 + kKeys - 1 <= pos)) {
+        // elsewhere, a bit per key of a chunk
+        if (t < whole0 || t >= whole1) {
           auto below = [](int x) { return (1u << min(max(x, 0), kChunkKeys)) - 1u; };   // the first x keys
 #pragma unroll
           for (int ch = 0; ch < kStepChunks; ++ch) {
@@ -887,8 +895,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) mx4[j] = max3(mx4[j], sv[e + j], sv[e + 4 + j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx4[j] = fmaxf(mx4[j], sv[60 + j]);
-        const float mx = fmaf(qe, fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]), lv);
+        for (int j = 0; j < 4; ++j) mx4[j] = max3(mx4[j], sv[60 + j], sv[60 + j]);
+        const float mx = fmaf(qe, max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]), lv);
         const bool move = mx > m_ref + kRescaleLog2;
         const bool scale = move && t > 0 && m_ref != -CUDART_INF_F;   // O holds earlier steps
         if (__any_sync(FULL, scale)) {
@@ -945,11 +953,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         mbar_arrive(smem_u32(&p_full[i]));
         sp.next();
         at.next();
-        if (BS) av.next();
+        if (kFp8) av.next();
       }
       for (int t = ntx; t < u.steps; ++t) {   // the stream's steps of the other tile
         at.next();
-        if (BS) av.next();
+        if (kFp8) av.next();
       }
       if (ok && ntx > 0) {
         // the row's factor for the helpers, who are done with the unit before

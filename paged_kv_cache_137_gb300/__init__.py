@@ -219,7 +219,7 @@ def _i64p(a: np.ndarray):
 
 def _stream(stream) -> int | None:
     if stream is None:  # the raw handle: building a Stream object costs more than a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -789,68 +789,77 @@ def empty_block_scales(desc: pkv_kv_desc, device="cuda") -> torch.Tensor:
     return torch.zeros((desc.num_blocks, desc.num_kv_heads, 2), dtype=torch.float32, device=device)
 
 
-def _scales(block_scales, desc):
-    t = block_scales
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous()
-            or t.shape != (desc.num_blocks, desc.num_kv_heads, 2)):
-        raise ValueError("block_scales must be a contiguous float32 CUDA tensor [num_blocks, num_kv_heads, 2]")
-    return t.data_ptr()
+def _on(t, name: str, dtype, shape, device: int) -> int:
+    """Address of a contiguous tensor of this dtype and shape on the current
+    device (one test on the way of every call, the reason only on a failure)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current "
+                     f"CUDA device")
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype, n, heads, d):
+def _rows_of(t, name: str, dtype, n, heads, d, device: int):
     """(address, elements between tokens) of [n, heads, d] whose tokens may lie
     apart (a view of a packed projection)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.shape != (n, heads, d) or (n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
-        raise ValueError(f"{name} must be [{n}, {heads}, {d}] with contiguous token rows")
-    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d)
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be a {dtype} tensor [{n}, {heads}, {d}] on the current CUDA device")
+    s = t.stride()
+    if n and (s[2] != 1 or (heads > 1 and s[1] != d)):
+        raise ValueError(f"{name}: a token's [{heads}, {d}] must be contiguous")
+    return t.data_ptr(), (s[0] if n > 1 else heads * d)
 
 
-def _cache_args(k_cache, v_cache, desc):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or tuple(t.shape) != desc.cache_shape:
-            raise ValueError(f"{name} must be {desc.torch_dtype}{desc.cache_shape}")
-    return _dev(k_cache, "k_cache", desc.torch_dtype), _dev(v_cache, "v_cache", desc.torch_dtype)
+def _scales(block_scales, desc, device: int) -> int:
+    return _on(block_scales, "block_scales", torch.float32, (desc.num_blocks, desc.num_kv_heads, 2), device)
+
+
+def _tables(block_tables, context_lens, device: int):
+    """(tables, max_blocks, lengths) addresses and the number of sequences."""
+    b = context_lens.shape[0]
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be int32[B, max_blocks]")
+    m = block_tables.shape[1]
+    return (_on(block_tables, "block_tables", torch.int32, (b, m), device), m,
+            _on(context_lens, "context_lens", torch.int32, (b,), device)), b
+
+
+def _longest(query_start, b) -> int:
+    return int((query_start[1:] - query_start[:-1]).max().item()) if b else 0
 
 
 def _append_args(k_cache, v_cache, k, v, block_tables, context_lens, desc, query_start, max_query_len, rope,
                  q, q_out, block_scales, k_inv_scale, v_inv_scale):
-    n, b = k.shape[0], context_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.dim() != 1:
-        raise ValueError("block_tables int32[B, max_blocks], context_lens int32[B] expected")
+    dev = torch._C._cuda_getDevice()
+    n, dtype, h, d = k.shape[0], k.dtype, desc.num_kv_heads, desc.head_dim
+    (tp, m, cp), b = _tables(block_tables, context_lens, dev)
     if query_start is None:
         if n != b:
             raise ValueError("without query_start there is one token per sequence")
         if max_query_len is not None and max_query_len < 1:
             raise ValueError("max_query_len must be at least 1")
-        longest = 1
+        sp, longest = None, 1
     else:
-        if query_start.shape != (b + 1,):
-            raise ValueError("query_start must be int32[B + 1]")
-        longest = max_query_len
-        if longest is None:
-            longest = int((query_start[1:] - query_start[:-1]).max().item()) if b else 0
-    dtype = k.dtype
-    h, d = desc.num_kv_heads, desc.head_dim
-    kc, vc = _cache_args(k_cache, v_cache, desc)
-    kp, ks = _token_rows(k, "k", dtype, n, h, d)
-    vp, vs = _token_rows(v, "v", dtype, n, h, d)
+        sp = _on(query_start, "query_start", torch.int32, (b + 1,), dev)
+        longest = _longest(query_start, b) if max_query_len is None else int(max_query_len)
+    shape, kind = desc.cache_shape, desc.torch_dtype
+    kc, vc = _on(k_cache, "k_cache", kind, shape, dev), _on(v_cache, "v_cache", kind, shape, dev)
+    kp, ks = _rows_of(k, "k", dtype, n, h, d, dev)
+    vp, vs = _rows_of(v, "v", dtype, n, h, d, dev)
     qp, qs, op, hq = None, 0, None, 0
     if q is not None:
         hq = q.shape[1]
-        qp, qs = _token_rows(q, "q", dtype, n, hq, d)
-        if q_out is None or q_out.shape != q.shape or q_out.dtype != dtype:
-            raise ValueError("q_out must match q")
-        op = _dev(q_out, "q_out")
+        qp, qs = _rows_of(q, "q", dtype, n, hq, d, dev)
+        op = _on(q_out, "q_out", dtype, (n, hq, d), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    return (kc, vc, None if block_scales is None else _scales(block_scales, desc), kp, ks, vp, vs, op, qp, qs, hq,
-            _dtype_code(k), _dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-            _dev(context_lens, "context_lens", torch.int32),
-            None if query_start is None else _dev(query_start, "query_start", torch.int32), b, n, int(longest),
-            None if rope is None else ctypes.byref(rope), ctypes.byref(desc), float(k_inv_scale),
-            float(v_inv_scale))
+    if rope is not None and rope._cos_sin.get_device() != dev:
+        raise ValueError("the rotation's table must be on the current CUDA device")
+    return (kc, vc, None if block_scales is None else _scales(block_scales, desc, dev), kp, ks, vp, vs, op, qp, qs,
+            hq, _dtype_code(k), tp, m, cp, sp, b, n, longest, None if rope is None else ctypes.byref(rope),
+            ctypes.byref(desc), k_inv_scale, v_inv_scale)
 
 
 def pkv_append(k_cache, v_cache, k, v, block_tables, context_lens, desc: pkv_kv_desc, query_start=None,
@@ -882,7 +891,8 @@ def pkv_copy_block_scales(block_scales, src_dst, desc: pkv_kv_desc, stream=None)
     pairs = np.ascontiguousarray(np.asarray(src_dst, dtype=np.int32).reshape(-1))
     if len(pairs) == 0:
         return
-    ptrs = (_P * len(block_scales))(*[_scales(t, desc) for t in block_scales])
+    dev = torch._C._cuda_getDevice()
+    ptrs = (_P * len(block_scales))(*[_scales(t, desc, dev) for t in block_scales])
     _check(lib().pkv_copy_block_scales(ptrs, len(block_scales), _i32p(pairs), len(pairs) // 2,
                                        ctypes.byref(desc), _stream(stream)))
 
@@ -902,19 +912,19 @@ def window_workspace_for(num_seqs, num_q_heads, max_blocks, desc, window_tokens=
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
-def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc):
-    """The arguments up to the tables of the windowed and block-scaled calls,
-    checked: (out, q, dtype, k, v), (tables, max_blocks, lengths), sequences, heads."""
+def _attention_args(out, q, k_cache, v_cache, block_scales, block_tables, context_lens, desc):
+    """The arguments up to the context lengths of the windowed and block-scaled
+    calls, checked, and the numbers of sequences, query rows and heads."""
+    dev = torch._C._cuda_getDevice()
     n, hq, d = q.shape
-    if out.shape != q.shape or out.dtype != q.dtype or d != desc.head_dim:
-        raise ValueError("out must match q [rows, Hq, head_dim]")
-    b = context_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.dim() != 1:
-        raise ValueError("block_tables int32[B, max_blocks], context_lens int32[B] expected")
-    kc, vc = _cache_args(k_cache, v_cache, desc)
-    return ((_dev(out, "out"), _dev(q, "q"), _dtype_code(q), kc, vc),
-            (_dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-             _dev(context_lens, "context_lens", torch.int32)), b, hq)
+    rows = (n, hq, desc.head_dim)
+    tab, b = _tables(block_tables, context_lens, dev)
+    shape, kind = desc.cache_shape, desc.torch_dtype
+    head = (_on(out, "out", q.dtype, rows, dev), _on(q, "q", q.dtype, rows, dev), _dtype_code(q),
+            _on(k_cache, "k_cache", kind, shape, dev), _on(v_cache, "v_cache", kind, shape, dev))
+    if block_scales is not None:
+        head += (_scales(block_scales, desc, dev),)
+    return head + tab, b, n, hq
 
 
 def pkv_attention_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, desc: pkv_kv_desc,
@@ -923,12 +933,12 @@ def pkv_attention_decode_window(out, q, k_cache, v_cache, block_tables, context_
     """Decode attention of q [B, Hq, D] over each context's last window_tokens
     positions and its first sink_tokens (pkv_attention_decode_window); the
     workspace is window_workspace_for's."""
-    head, tab, b, hq = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc)
-    if q.shape[0] != b:
+    args, b, n, hq = _attention_args(out, q, k_cache, v_cache, None, block_tables, context_lens, desc)
+    if n != b:
         raise ValueError("one query per sequence expected")
     _check(lib().pkv_attention_decode_window(
-        *head, *tab, b, hq, ctypes.byref(desc), int(window_tokens), int(sink_tokens), float(softmax_scale),
-        float(k_scale), float(v_scale), int(partition_tokens), *_ws(workspace), _stream(stream)))
+        *args, b, hq, ctypes.byref(desc), window_tokens, sink_tokens, softmax_scale, k_scale, v_scale,
+        partition_tokens, *_ws(workspace), _stream(stream)))
     return out
 
 
@@ -937,23 +947,24 @@ def pkv_attention_decode_block_scaled(out, q, k_cache, v_cache, block_scales, bl
                                       partition_tokens=0, workspace=None, stream=None):
     """Decode attention over an E4M3 cache with a scale per (block, KV head)
     (pkv_attention_decode_block_scaled); window_tokens 0 sees the whole context."""
-    head, tab, b, hq = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc)
-    if q.shape[0] != b:
+    if block_scales is None:
+        raise ValueError("block_scales is None")
+    args, b, n, hq = _attention_args(out, q, k_cache, v_cache, block_scales, block_tables, context_lens, desc)
+    if n != b:
         raise ValueError("one query per sequence expected")
     _check(lib().pkv_attention_decode_block_scaled(
-        *head, _scales(block_scales, desc), *tab, b, hq, ctypes.byref(desc), int(window_tokens),
-        int(sink_tokens), float(softmax_scale), int(partition_tokens), *_ws(workspace), _stream(stream)))
+        *args, b, hq, ctypes.byref(desc), window_tokens, sink_tokens, softmax_scale, partition_tokens,
+        *_ws(workspace), _stream(stream)))
     return out
 
 
-def _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, desc, max_query_len):
-    head, tab, b, hq = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, desc)
-    if query_start.shape != (b + 1,):
-        raise ValueError("query_start must be int32[B + 1]")
+def _prefill_args(out, q, k_cache, v_cache, block_scales, block_tables, context_lens, query_start, desc,
+                  max_query_len):
+    args, b, n, hq = _attention_args(out, q, k_cache, v_cache, block_scales, block_tables, context_lens, desc)
+    start = _on(query_start, "query_start", torch.int32, (b + 1,), torch._C._cuda_getDevice())
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if b else 0
-    return head, (*tab, _dev(query_start, "query_start", torch.int32), b, q.shape[0], int(max_query_len), hq,
-                  ctypes.byref(desc))
+        max_query_len = _longest(query_start, b)
+    return args + (start, b, n, int(max_query_len), hq, ctypes.byref(desc))
 
 
 def pkv_attention_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
@@ -962,11 +973,10 @@ def pkv_attention_prefill_window(out, q, k_cache, v_cache, block_tables, context
     """Prefill attention of packed chunks q [total_q, Hq, D], each query over
     its last window_tokens positions and the first sink_tokens
     (pkv_attention_prefill_window); otherwise as pkv_attention_prefill."""
-    head, rest = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, desc,
-                               max_query_len)
-    _check(lib().pkv_attention_prefill_window(
-        *head, *rest, int(window_tokens), int(sink_tokens), float(softmax_scale), float(k_scale),
-        float(v_scale), _stream(stream)))
+    args = _prefill_args(out, q, k_cache, v_cache, None, block_tables, context_lens, query_start, desc,
+                         max_query_len)
+    _check(lib().pkv_attention_prefill_window(*args, window_tokens, sink_tokens, softmax_scale, k_scale, v_scale,
+                                              _stream(stream)))
     return out
 
 
@@ -975,11 +985,12 @@ def pkv_attention_prefill_block_scaled(out, q, k_cache, v_cache, block_scales, b
                                        window_tokens=0, sink_tokens=0, stream=None):
     """Prefill attention over an E4M3 cache with a scale per (block, KV head)
     (pkv_attention_prefill_block_scaled); window_tokens 0 sees the whole context."""
-    head, rest = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, desc,
-                               max_query_len)
-    _check(lib().pkv_attention_prefill_block_scaled(
-        *head, _scales(block_scales, desc), *rest, int(window_tokens), int(sink_tokens), float(softmax_scale),
-        _stream(stream)))
+    if block_scales is None:
+        raise ValueError("block_scales is None")
+    args = _prefill_args(out, q, k_cache, v_cache, block_scales, block_tables, context_lens, query_start, desc,
+                         max_query_len)
+    _check(lib().pkv_attention_prefill_block_scaled(*args, window_tokens, sink_tokens, softmax_scale,
+                                                    _stream(stream)))
     return out
 
 

@@ -17,7 +17,8 @@ int window_ctas_per_sm(const pkv_kv_desc* d, int group) {
 
 namespace {
 
-constexpr int kMinPart = 256, kMaxPart = 8192, kMultiWavePart = 4096;
+constexpr int kMinPart = 1024, kMultiWavePart = 4096;
+constexpr int kMaxPart = 1 << 20;   // a multiple of 64
 
 int sm_count() {
   static std::atomic<int> cache[64];
@@ -39,7 +40,9 @@ int sm_count() {
 // What a call decides before it launches.
 struct WindowPlan {
   int32_t part = 0;     // tokens per split, a multiple of 64
-  int64_t splits = 1;   // of the longest span the arguments allow
+  int64_t seen = 0;     // tokens of the longest span the arguments allow (whole chunks)
+  int64_t splits = 1;   // of that span
+  bool alike = false;   // most spans are that long: a window over longer contexts
   size_t m_off = 0, l_off = 0, acc_off = 0, bytes = 0;   // workspace (counters first)
 };
 
@@ -58,26 +61,43 @@ pkv_status plan_window(const pkv_kv_desc* d, int32_t num_seqs, int32_t num_q_hea
   int64_t chunks = (max_ctx + 15) / 16;
   if (window > 0)
     chunks = std::min(chunks, (static_cast<int64_t>(sinks) + 15) / 16 + (static_cast<int64_t>(window) + 15) / 16 + 1);
+  p.seen = chunks * 16;
+  p.alike = window > 0 && max_ctx >= 2 * p.seen;
   if (requested > 0) {
     p.part = requested;
   } else {
-    // The fewest tokens per split for which the expected units fill one wave
-    // of resident CTAs: lengths are expected to spread evenly up to max_ctx,
-    // of which min(length, seen) tokens are read, seen - seen^2 / (2 max_ctx)
-    // on average, and each pair's last split to be half full.  With more
-    // pairs than two waves the hardware balances the waves itself and only
-    // the longest spans are split in two.
-    const int64_t slots = static_cast<int64_t>(sm_count()) * window_ctas_per_sm(d, num_q_heads / d->num_kv_heads);
+    // A merge of splits costs the call about 4 us (partials, a fence, the
+    // arrival count, the gather), and a hundred units draw the whole
+    // bandwidth, so splits are made for three reasons only:
+    //  * fewer (sequence, KV head) pairs than half the SMs: as many splits as
+    //    fill the SMs, of at least 1,024 tokens (32 pairs of 4,100 tokens: 19.3
+    //    us in four, 29.1 in one; 64 of 1,028: 13.7 us in two, 12.9 in one);
+    //  * lengths that vary widely over less than two waves of resident CTAs:
+    //    about one wave of units (256 pairs of up to 4,096 tokens: 39 to 41 us
+    //    in three, 40 to 42 in one; with longer contexts the longest unit
+    //    alone would set the end).  Spans that a window makes alike stay whole
+    //    (192 pairs of 2,052 tokens: 35.9 us, 41.3 in two);
+    //  * more pairs than two waves: only the longest spans in two (1,024 pairs
+    //    of up to 4,096 tokens: 106 us, 111 whole).
+    const int64_t sms = sm_count();
+    const int64_t slots = sms * window_ctas_per_sm(d, num_q_heads / d->num_kv_heads);
     const int64_t pairs = static_cast<int64_t>(num_seqs) * d->num_kv_heads;
-    const int64_t seen = std::max<int64_t>(chunks * 16, 1);
-    int64_t t;
-    if (2 * slots <= pairs + 2) {
+    const int64_t seen = p.seen;
+    const bool alike = p.alike;
+    int64_t t = seen;
+    if (2 * pairs <= sms) {
+      const int64_t n = std::max<int64_t>(1, std::min<int64_t>(sms / pairs, seen / kMinPart));
+      t = (seen + n - 1) / n;
+    } else if (2 * slots <= pairs + 2) {
       t = std::max<int64_t>(kMultiWavePart, (seen + 1) / 2);
-    } else {
+    } else if (!alike) {
+      // the mean of min(length, seen) over lengths spread evenly up to
+      // max_ctx; each pair's last split is half full
       const double mean = static_cast<double>(seen) - 0.5 * static_cast<double>(seen) * seen / std::max<int64_t>(max_ctx, 1);
-      t = std::max<int64_t>(kMinPart, static_cast<int64_t>(pairs * mean / (slots - pairs / 2)) + 1);
+      const double room = std::max(0.85 * slots - 0.5 * pairs, 0.25 * pairs);
+      t = std::max<int64_t>(kMinPart, static_cast<int64_t>(pairs * mean / room) + 1);
     }
-    p.part = static_cast<int32_t>(std::min<int64_t>(kMaxPart, (t + 63) / 64 * 64));
+    p.part = static_cast<int32_t>(std::min<int64_t>(kMaxPart, (std::max<int64_t>(t, 1) + 63) / 64 * 64));
   }
   const int64_t part_chunks = p.part / 16;
   p.splits = std::max<int64_t>(1, (chunks + part_chunks - 1) / part_chunks);
@@ -169,6 +189,17 @@ pkv_status decode_window_impl(void* out, const void* q, int32_t q_dtype, const v
   a.partition = plan.part;
   a.part_chunks = plan.part / 16;
   a.max_splits = static_cast<int32_t>(plan.splits);
+  const int64_t units = static_cast<int64_t>(num_seqs) * desc->num_kv_heads * plan.splits;
+  a.ctas_per_sm = static_cast<int32_t>(std::min<int64_t>((units + sm_count() - 1) / sm_count(), 4));
+  // a unit of few chunks gains nothing from more warps, and each adds to the
+  // merge (128 tokens: 4.3 us with four, 5.6 with sixteen)
+  const int64_t unit_tokens = plan.seen / plan.splits;
+  if (unit_tokens <= 256) a.ctas_per_sm = std::max(a.ctas_per_sm, 3);
+  else if (unit_tokens <= 512) a.ctas_per_sm = std::max(a.ctas_per_sm, 2);
+  // more than one wave of units alike: two CTAs of six warps finish a last
+  // unit sooner than one of four left alone (512 units of 1,028 tokens: 49 us,
+  // 56 with three CTAs of four)
+  else if (plan.alike && units > 3 * static_cast<int64_t>(sm_count())) a.ctas_per_sm = 2;
   const bool tensor_scales = fp8 && !block_scales;
   a.qk_scale = softmax_scale * (tensor_scales ? k_scale : 1.0f) * 1.4426950408889634f;
   a.v_scale = tensor_scales ? v_scale : 1.0f;

@@ -21,11 +21,10 @@
 // of 9 to 16 heads keep two column sets per K and V fragment.
 //
 // A chunk lies in one block, so its two scales are scalars.  The K scale joins
-// the logit scale.  The V scale vs joins the exponent of P, with a reference
-// of its own: O is kept in units of 2^mo, mo the running maximum of
-// s + log2(vs), so that P = 2^(s + log2(vs) - mo) <= 1 keeps all the bits of
-// its 16-bit form however far the blocks' scales lie apart; the sum l stays in
-// units of 2^m, m the running maximum of s, and o = O 2^(mo - m) / l.
+// the logit scale.  The V scale vs joins the exponent of P: with m the running
+// maximum of s + log2(vs), P = 2^(s + log2(vs) - m) <= 1 keeps all the bits of
+// its 16-bit form however far the blocks' scales lie apart, and the row sum
+// takes P / vs, so that O and l keep one reference.
 //
 // Sums, maxima and O are fp32; q and P are rounded to the MMA's 16-bit type
 // (the cache's, f16 for E4M3), off by a relative 2^-8 (bf16) or 2^-11 (f16) at
@@ -65,11 +64,10 @@ struct Span {
 
 // A warp's running softmax state of 8 * NH heads (lane (g, q4): heads
 // 8 nh + 2 q4 + j, O^T rows g and g + 8 of each 16-row tile).
-template <int D, int NH, bool BS>
+template <int D, int NH>
 struct WindowState {
   float o[NH][D / 16][4];
   float m[NH][2], l[NH][2];
-  float mo[BS ? NH : 1][2];   // the reference of O where blocks have scales
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -77,19 +75,29 @@ struct WindowState {
       for (int n = 0; n < D / 16; ++n) o[h][n][0] = o[h][n][1] = o[h][n][2] = o[h][n][3] = 0.f;
       m[h][0] = m[h][1] = -CUDART_INF_F;
       l[h][0] = l[h][1] = 0.f;
-      if (BS) mo[h][0] = mo[h][1] = -CUDART_INF_F;
     }
   }
 };
 
+// 2^x by the hardware approximation (relative error about 2^-22, 0 at -inf).
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A block scale within the range it is promised in.
+__device__ __forceinline__ float block_scale(float x) {
+  return fminf(fmaxf(x, 9.094947017729282e-13f), 1099511627776.f);   // 2^-40, 2^40
+}
 __device__ __forceinline__ float finite_or_0(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
 // One chunk folded into the state; kt, vt: its 16 rows of K and V, pos: the
-// position of row 0, qk: logit scale (log2 domain), vs: the block's V scale.
+// position of row 0, qk: logit scale (log2 domain), vs: the block's V scale
+// (BS).
 // Returns true if V rows were zeroed (generic writes the caller fences before
 // TMA refills the stage).
 template <typename KV, int D, int NH, bool BS>
-__device__ __forceinline__ bool chunk_step(WindowState<D, NH, BS>& st,
+__device__ __forceinline__ bool chunk_step(WindowState<D, NH>& st,
                                            const uint32_t (&qb)[NH][D / 16][2], const uint8_t* kt,
                                            uint8_t* vt, const Span& span, int pos, float qk, float vs,
                                            int lane) {
@@ -115,16 +123,20 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH, BS>& st,
   const int rk = (mi & 1) * 8 + li;
 
   // S^T = K q^T
-  float sc[NH][4];
+  // (in two chains of half the length: one warp's MMAs are latency)
+  float sc[NH][4], sd[NH][4];
 #pragma unroll
-  for (int h = 0; h < NH; ++h) sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
+  for (int h = 0; h < NH; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[h][e] = sd[h][e] = 0.f;
   if constexpr (!kFp8) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t a0, a1, a2, a3;
       ldsm_x4(kbase + swz<S>(rk, 2 * ks + (mi >> 1)), a0, a1, a2, a3);
 #pragma unroll
-      for (int h = 0; h < NH; ++h) mma16816<kBf>(sc[h], a0, a1, a2, a3, qb[h][ks][0], qb[h][ks][1]);
+      for (int h = 0; h < NH; ++h)
+        mma16816<kBf>(ks & 1 ? sd[h] : sc[h], a0, a1, a2, a3, qb[h][ks][0], qb[h][ks][1]);
     }
   } else {
 #pragma unroll
@@ -137,14 +149,18 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH, BS>& st,
         const uint32_t a2 = e4m3x2_f16x2(w[2 * k] >> 16), a3 = e4m3x2_f16x2(w[2 * k + 1] >> 16);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-          mma16816<false>(sc[h], a0, a1, a2, a3, qb[h][ks + k][0], qb[h][ks + k][1]);
+          mma16816<false>(k ? sd[h] : sc[h], a0, a1, a2, a3, qb[h][ks + k][0], qb[h][ks + k][1]);
       }
     }
   }
+#pragma unroll
+  for (int h = 0; h < NH; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[h][e] += sd[h][e];
 
   // online softmax over the tokens (rows g, g + 8) of heads 2 q4 + j
   const bool see0 = whole || span.sees(pos + g), see1 = whole || span.sees(pos + g + 8);
-  const float lv = BS ? __log2f(vs) : 0.f;
+  const float lv = BS ? __log2f(vs) : 0.f, inv_v = BS ? __frcp_rn(vs) : 1.f;
   uint32_t pb[NH][2];
   float corr[NH][2];
   bool moved = false;
@@ -153,30 +169,19 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH, BS>& st,
     float p[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float v0 = see0 ? sc[h][j] * qk : -CUDART_INF_F;
-      const float v1 = see1 ? sc[h][2 + j] * qk : -CUDART_INF_F;
+      const float v0 = see0 ? fmaf(sc[h][j], qk, lv) : -CUDART_INF_F;
+      const float v1 = see1 ? fmaf(sc[h][2 + j], qk, lv) : -CUDART_INF_F;
       float mx = fmaxf(v0, v1);
       mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
       const float mn = fmaxf(st.m[h][j], mx);
       const float ref = finite_or_0(mn);   // every logit so far -inf: all weights 0
-      const float c = exp2f(st.m[h][j] - ref);
-      const float e0 = exp2f(v0 - ref), e1 = exp2f(v1 - ref);
+      corr[h][j] = ex2_approx(st.m[h][j] - ref);
+      p[j] = ex2_approx(v0 - ref);
+      p[2 + j] = ex2_approx(v1 - ref);
       st.m[h][j] = mn;
-      st.l[h][j] = st.l[h][j] * c + (e0 + e1);
-      if constexpr (BS) {
-        const float mon = fmaxf(st.mo[h][j], mx + lv);
-        const float oref = finite_or_0(mon);
-        corr[h][j] = exp2f(st.mo[h][j] - oref);
-        st.mo[h][j] = mon;
-        p[j] = exp2f(v0 + lv - oref);
-        p[2 + j] = exp2f(v1 + lv - oref);
-      } else {
-        corr[h][j] = c;
-        p[j] = e0;
-        p[2 + j] = e1;
-      }
+      st.l[h][j] = st.l[h][j] * corr[h][j] + (p[j] + p[2 + j]) * inv_v;
       moved = moved || corr[h][j] != 1.f;
     }
     // P^T as the B operand: the transposes of its two 8 x 8 blocks
@@ -226,15 +231,14 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH, BS>& st,
 }
 
 // The state to the merge buffers mS, lS [warp][16], oS [warp][16][D] (heads <
-// G), O brought to the reference of l.
-template <typename KV, int D, int NH, bool BS>
-__device__ __forceinline__ void publish_window(const WindowState<D, NH, BS>& st, float* mS, float* lS,
+// G).
+template <typename KV, int D, int NH>
+__device__ __forceinline__ void publish_window(const WindowState<D, NH>& st, float* mS, float* lS,
                                                float* oS, int warp, int G, int lane) {
   constexpr bool kFp8 = std::is_same<KV, E4M3>::value;
   const int g = lane >> 2, q4 = lane & 3;
 #pragma unroll
   for (int h = 0; h < NH; ++h) {
-    float f[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float l = st.l[h][j];
@@ -245,24 +249,22 @@ __device__ __forceinline__ void publish_window(const WindowState<D, NH, BS>& st,
         mS[warp * 16 + 8 * h + 2 * q4 + j] = l == l ? st.m[h][j] : 0.f;
         lS[warp * 16 + 8 * h + 2 * q4 + j] = l;
       }
-      f[j] = BS && st.m[h][j] != -CUDART_INF_F ? exp2f(st.mo[h][j] - st.m[h][j]) : 1.f;
     }
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int head = 8 * h + 2 * q4 + (e & 1);
-        if (head < G)
-          oS[(warp * 16 + head) * D + out_row_t<kFp8>(mt, g, e >> 1)] = st.o[h][mt][e] * f[e & 1];
+        if (head < G) oS[(warp * 16 + head) * D + out_row_t<kFp8>(mt, g, e >> 1)] = st.o[h][mt][e];
       }
   }
 }
 
-// Write the CTA's combined state (the four warps' in mS, lS, oS): the output
+// Write the CTA's combined state (its W warps' in mS, lS, oS): the output
 // of a lone split, else the split's partial; the last split of the pair to
 // arrive (an atomic count, never a wait) merges them all in split order.
 // stage: `cap` floats of shared memory the merge may use.
-template <typename Q, int D>
+template <typename Q, int D, int W>
 __device__ __forceinline__ void finish_unit(const WindowArgs& a, const float* mS, const float* lS,
                                             const float* oS, int kvh, int seq, int split, int nsplit,
                                             int bad_bits, float v_scale, float* stage, int cap,
@@ -270,10 +272,10 @@ __device__ __forceinline__ void finish_unit(const WindowArgs& a, const float* mS
   const int tid = threadIdx.x, G = a.group;
   const size_t head0 = static_cast<size_t>(seq) * a.num_q_heads + static_cast<size_t>(kvh) * G;
   if (tid == 0 && bad_bits != 0 && a.status != nullptr) atomicOr(a.status, bad_bits);
-  for (int i = tid; i < G * D; i += kThreads) {
+  for (int i = tid; i < G * D; i += 32 * W) {
     const int row = i / D, d = i % D;
     float M, L, A;
-    combine_warps(mS, lS, oS, kWarps, 16, row, d, D, M, L, A);
+    combine_warps(mS, lS, oS, W, 16, row, d, D, M, L, A);
     A *= v_scale;
     if (nsplit == 1) {
       const float o = bad_bits ? CUDART_NAN_F : (L > 0.f || L != L) ? A / L : 0.f;
@@ -295,18 +297,30 @@ __device__ __forceinline__ void finish_unit(const WindowArgs& a, const float* mS
   __syncthreads();
   if (!*s_last) return;
   __threadfence();
-  merge_splits<Q, D, kThreads>(a, head0, nsplit, a.max_splits, 0, stage, cap);
+  merge_splits<Q, D, 32 * W>(a, head0, nsplit, a.max_splits, 0, stage, cap);
   if (tid == 0) atomicExch(counter, 0);
 }
 
+// Warps per CTA by the CTAs of the call that share an SM: a chunk is about a
+// microsecond of one warp's latency, so an SM wants its 12 (rows of 256 bytes:
+// rings of 16 KiB a warp) or 16 warps (12 KiB) whether its work is one unit or
+// several.  The rings take 192 KiB of an SM either way.
+template <typename KV, int D, int NH>
+constexpr int window_warps(int c) {
+  // (two column sets of heads leave registers for 12 warps as well)
+  constexpr bool wide = NH > 1 || Geom<KV, D, 1>::kStageBytes >= 8192;
+  return c <= 1 ? (wide ? 12 : 16) : c == 2 ? (wide ? 6 : 8) : kWarps;
+}
 template <typename KV, int D>
 constexpr int window_stages() { return Geom<KV, D, 1>::kStageBytes >= 8192 ? 2 : 3; }
-// Resident CTAs per SM the kernel is compiled for (64 KiB or 48 KiB of ring).
-template <typename KV, int D, int NH>
-constexpr int window_ctas() { return NH == 1 && Geom<KV, D, 1>::kStageBytes < 8192 ? 4 : 3; }
+template <typename KV, int D, int NH, int W>
+constexpr int window_ctas() {
+  constexpr int warps = NH == 1 && Geom<KV, D, 1>::kStageBytes < 8192 ? 16 : 12;
+  return warps / W < 1 ? 1 : warps / W;
+}
 
-template <typename KV, typename Q, int D, int NH, bool BS>
-__global__ void __launch_bounds__(kThreads, window_ctas<KV, D, NH>())
+template <typename KV, typename Q, int D, int NH, bool BS, int W>
+__global__ void __launch_bounds__(32 * W, window_ctas<KV, D, NH, W>())
     decode_window_kernel(const WindowArgs a, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap) {
   using G_ = Geom<KV, D, 1>;   // one warp's stage: 16 tokens of K, then of V
@@ -338,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, window_ctas<KV, D, NH>())
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t s_bar[kWarps][NS];
-  __shared__ int s_bad[kWarps], s_last;
+  __shared__ uint64_t s_bar[W][NS];
+  __shared__ int s_bad[W], s_last;
   uint8_t* ring = smem + warp * NS * G_::kStageBytes;
   uint64_t* bar = s_bar[warp];
   if (lane < NS) mbar_init(smem_u32(&bar[lane]), 1);
@@ -351,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, window_ctas<KV, D, NH>())
   const int64_t n_all = span.n;
   const int c0 = static_cast<int>(split * n_all / nsplit);
   const int c1 = static_cast<int>((split + 1) * n_all / nsplit);
-  const int wa = c0 + warp * (c1 - c0) / kWarps;
-  const int n = c0 + (warp + 1) * (c1 - c0) / kWarps - wa;
+  const int wa = c0 + warp * (c1 - c0) / W;
+  const int n = c0 + (warp + 1) * (c1 - c0) / W - wa;
   const int32_t* trow = a.tables + static_cast<size_t>(seq) * a.max_blocks;
   int bad = bad_ctx ? kBadLength : 0;
   // lane l of batch b: the pool row (-1: a bad table entry) and the scales of
@@ -369,33 +383,37 @@ __global__ void __launch_bounds__(kThreads, window_ctas<KV, D, NH>())
     }
     const int slab = blk * a.num_kv_heads + kvh;
     row = slab * T + p % T;
-    if constexpr (BS) scales = *reinterpret_cast<const float2*>(a.block_scales + 2 * static_cast<size_t>(slab));
+    if constexpr (BS) {
+      const float2 x = *reinterpret_cast<const float2*>(a.block_scales + 2 * static_cast<size_t>(slab));
+      scales = make_float2(block_scale(x.x), block_scale(x.y));
+    }
   };
   int row_cur = -1, row_nxt = -1;
   float2 sc_cur = make_float2(0.f, 0.f), sc_nxt = sc_cur;
   fetch(0, row_cur, sc_cur);
-  auto issue = [&](int i, int base) {   // base: the first chunk of the current batch
+  auto issue = [&](int i, int base, int slot) {   // base: the first chunk of the current batch
     const int row = __shfl_sync(FULL, i - base < 32 ? row_cur : row_nxt, i & 31);
-    const uint32_t b = smem_u32(&bar[i % NS]);
+    const uint32_t b = smem_u32(&bar[slot]);
     if (lane == 0) mbar_arrive_expect_tx(b, row >= 0 ? G_::kStageBytes : 0);
     __syncwarp();
     if (lane < 2 && row >= 0)
-      tma_box<KV, D>(smem_u32(ring + (i % NS) * G_::kStageBytes + lane * G_::kTileBytes),
+      tma_box<KV, D>(smem_u32(ring + slot * G_::kStageBytes + lane * G_::kTileBytes),
                      lane ? &vmap : &kmap, row, b);
   };
-  for (int i = 0; i < NS && i < n; ++i) issue(i, 0);
+  for (int i = 0; i < NS && i < n; ++i) issue(i, 0, i);
   fetch(1, row_nxt, sc_nxt);
 
-  WindowState<D, NH, BS> st;
+  WindowState<D, NH> st;
   st.reset();
+  int s = 0;
+  uint32_t par = 0;
   for (int i = 0; i < n; ++i) {
     if ((i & 31) == 0 && i > 0) {
       row_cur = row_nxt;
       sc_cur = sc_nxt;
       fetch(i / 32 + 1, row_nxt, sc_nxt);
     }
-    const int s = i % NS;
-    if (!__all_sync(FULL, stage_wait(smem_u32(&bar[s]), (i / NS) & 1, a.wait_ns))) {
+    if (!__all_sync(FULL, stage_wait(smem_u32(&bar[s]), par, a.wait_ns))) {
       // wait (bounded) for the copies still in flight before the ring is reused
       bad |= kTimeout;
       if (lane == 0)
@@ -415,29 +433,35 @@ __global__ void __launch_bounds__(kThreads, window_ctas<KV, D, NH>())
         fence_proxy_async();   // the zeroed rows, before TMA refills the stage
     }
     __syncwarp();
-    if (i + NS < n) issue(i + NS, i & ~31);
+    if (i + NS < n) issue(i + NS, i & ~31, s);
+    if (++s == NS) {
+      s = 0;
+      par ^= 1;
+    }
   }
 
   bad = __reduce_or_sync(FULL, bad);
   if (lane == 0) s_bad[warp] = bad;
   __syncthreads();   // every ring is idle: the merge takes its place
   float* mS = reinterpret_cast<float*>(smem);
-  float* lS = mS + kWarps * 16;
-  float* oS = lS + kWarps * 16;
-  constexpr int kCap = kWarps * NS * G_::kStageBytes / 4;
-  static_assert(kCap >= 2 * kWarps * 16 + kWarps * 16 * D, "the warp merge reuses the rings");
-  publish_window<KV, D, NH, BS>(st, mS, lS, oS, warp, G, lane);
+  float* lS = mS + W * 16;
+  float* oS = lS + W * 16;
+  constexpr int kCap = W * NS * G_::kStageBytes / 4;
+  static_assert(kCap >= 2 * W * 16 + W * 16 * D, "the warp merge reuses the rings");
+  publish_window<KV, D, NH>(st, mS, lS, oS, warp, G, lane);
   __syncthreads();
-  const int bad_bits = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
-  finish_unit<Q, D>(a, mS, lS, oS, kvh, seq, split, nsplit, bad_bits, hs.v,
-                    reinterpret_cast<float*>(smem), kCap, &s_last);
+  int bad_bits = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) bad_bits |= s_bad[w];
+  finish_unit<Q, D, W>(a, mS, lS, oS, kvh, seq, split, nsplit, bad_bits, hs.v,
+                       reinterpret_cast<float*>(smem), kCap, &s_last);
 }
 
-template <typename KV, typename Q, int D, int NH, bool BS>
+template <typename KV, typename Q, int D, int NH, bool BS, int W>
 pkv_status launch_window_form(const WindowArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               cudaStream_t st) {
-  constexpr int smem = kWarps * window_stages<KV, D>() * Geom<KV, D, 1>::kStageBytes + 1024;
-  auto kernel = decode_window_kernel<KV, Q, D, NH, BS>;
+  constexpr int smem = W * window_stages<KV, D>() * Geom<KV, D, 1>::kStageBytes + 1024;
+  auto kernel = decode_window_kernel<KV, Q, D, NH, BS, W>;
   static std::atomic<uint64_t> configured{0};   // the shared-memory opt-in is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -452,9 +476,19 @@ pkv_status launch_window_form(const WindowArgs& a, const CUtensorMap& kmap, cons
     configured.fetch_or(bit);
   }
   const dim3 grid(a.num_kv_heads, a.num_seqs, a.max_splits);
-  e = launch_dependent(kernel, grid, kThreads, smem, st, a, kmap, vmap);
+  e = launch_dependent(kernel, grid, 32 * W, smem, st, a, kmap, vmap);
   if (e != cudaSuccess) return cuda_fail("windowed decode: launch", e);
   return check_launch("windowed decode (tensor core)");
+}
+
+template <typename KV, typename Q, int D, int NH, bool BS>
+pkv_status launch_window_w(const WindowArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                           cudaStream_t st) {
+  if (a.ctas_per_sm <= 1)
+    return launch_window_form<KV, Q, D, NH, BS, window_warps<KV, D, NH>(1)>(a, kmap, vmap, st);
+  if (a.ctas_per_sm == 2)
+    return launch_window_form<KV, Q, D, NH, BS, window_warps<KV, D, NH>(2)>(a, kmap, vmap, st);
+  return launch_window_form<KV, Q, D, NH, BS, kWarps>(a, kmap, vmap, st);
 }
 
 template <typename KV, typename Q, int D>
@@ -462,11 +496,11 @@ pkv_status launch_window_d(const WindowArgs& a, const CUtensorMap& kmap, const C
                            cudaStream_t st) {
   if constexpr (std::is_same<KV, E4M3>::value) {
     if (a.block_scales)
-      return a.group <= 8 ? launch_window_form<KV, Q, D, 1, true>(a, kmap, vmap, st)
-                          : launch_window_form<KV, Q, D, 2, true>(a, kmap, vmap, st);
+      return a.group <= 8 ? launch_window_w<KV, Q, D, 1, true>(a, kmap, vmap, st)
+                          : launch_window_w<KV, Q, D, 2, true>(a, kmap, vmap, st);
   }
-  return a.group <= 8 ? launch_window_form<KV, Q, D, 1, false>(a, kmap, vmap, st)
-                      : launch_window_form<KV, Q, D, 2, false>(a, kmap, vmap, st);
+  return a.group <= 8 ? launch_window_w<KV, Q, D, 1, false>(a, kmap, vmap, st)
+                      : launch_window_w<KV, Q, D, 2, false>(a, kmap, vmap, st);
 }
 
 }  // namespace tc

@@ -12,6 +12,7 @@ struct WindowArgs : DecodeArgs {
   int32_t window;             // positions [ctx - window, ctx) are seen; 0: all of them
   int32_t sinks;              // and positions [0, sinks)
   int32_t part_chunks;        // 16-token chunks per split
+  int32_t ctas_per_sm;        // CTAs of this call that share an SM, at most
   const float* block_scales;  // [num_blocks][N_kv][2] (K, V), or NULL
 };
 

@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
     const size_t base = (slab * T + pos % T) * D;
     float ks = 1.f, vs = 1.f;
     if (a.block_scales) {
-      ks = a.block_scales[2 * slab];
-      vs = a.block_scales[2 * slab + 1];
+      ks = block_scale(a.block_scales[2 * slab]);
+      vs = block_scale(a.block_scales[2 * slab + 1]);
     }
     float s[GM];
 #pragma unroll
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
     for (int e = 0; e < DV; ++e) oS[(warp * 16 + j) * D + lane * DV + e] = acc[j][e];
   }
   __syncthreads();
-  finish_unit<Q, D>(a, mS, lS, oS, kvh, seq, split, nsplit, s_bad, hs.v, merge_s,
+  finish_unit<Q, D, kWarps>(a, mS, lS, oS, kvh, seq, split, nsplit, s_bad, hs.v, merge_s,
                     static_cast<int>(sizeof(merge_s) / sizeof(float)), &s_last);
 }
 

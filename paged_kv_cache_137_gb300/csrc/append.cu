@@ -24,10 +24,10 @@
 // that a rotation never leaves the thread; 16 (head_dim 128) or 32 tokens and
 // a group of rows share a CTA, and a thread keeps its angles in registers
 // while it walks the rows of its token.  A (block, KV head, K|V) of a
-// block-scaled cache is one warp's: the maximum is a warp reduction, and no
-// other warp writes that block's bytes or its scale.
+// block-scaled cache is one warp's (two for blocks of 32; D / 16 lanes where
+// there is one new token): the maximum is a reduction over its lanes, and
+// nobody else writes that block's bytes or its scale.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include <math_constants.h>
@@ -60,6 +60,7 @@ struct AppendArgs {
   int32_t rows_per_cta;      // rows (heads) a thread walks
   int32_t row_groups;
   int32_t row_ctas;          // CTAs of the row form in grid.x; the rest take block units
+  int32_t block_parts;       // CTAs of one touched block
   int* status;
 };
 
@@ -102,11 +103,59 @@ __device__ __forceinline__ Raw8<Tag> load_raw8(const void* base, size_t idx) {
   return r;
 }
 
-// x (8 elements at the unit's first place) and y (at its second) as fp32,
-// rotated by the 8 angles.  Half-split pairs are (x[i], y[i]); adjacent pairs
-// lie within x (angles 0-3) and within y (angles 4-7).
+// A thread's unit of a row: two groups of 8 elements, at p0 and p1, and how
+// they turn.  Neighbouring units hold neighbouring groups, so that a warp's
+// 16-byte accesses make whole 128-byte lines.  Half-split pairs join the two
+// groups; adjacent pairs lie within a group.
+struct UnitPlace {
+  int p0, p1;
+  bool t0, t1;   // the group is rotated (half-split: both or neither)
+};
+__device__ __forceinline__ UnitPlace unit_place(int u, int head_dim, int rotary, bool interleaved) {
+  UnitPlace w;
+  if (interleaved) {
+    w.p0 = 8 * u;
+    w.p1 = head_dim / 2 + 8 * u;
+    w.t0 = w.p0 < rotary;
+    w.t1 = w.p1 < rotary;
+  } else if (u < rotary / 16) {
+    w.p0 = 8 * u;
+    w.p1 = rotary / 2 + 8 * u;
+    w.t0 = w.t1 = true;
+  } else {
+    w.p0 = rotary + 8 * (u - rotary / 16);
+    w.p1 = w.p0 + (head_dim - rotary) / 2;
+    w.t0 = w.t1 = false;
+  }
+  return w;
+}
+
+// The unit's 8 angles at a position: half-split pair i of 8 (elements p0 + i
+// and p1 + i), or the four adjacent pairs of each group.
+__device__ __forceinline__ const float* angle_row(const AppendArgs& a, int pos) {
+  return a.angles + static_cast<size_t>(pos) * a.rotary;
+}
+__device__ __forceinline__ void load_angles(const AppendArgs& a, const float* row, const UnitPlace& w,
+                                            float (&c)[8], float (&s)[8]) {
+  const int half = a.rotary / 2;
+  if (a.interleaved) {
+    if (w.t0) {
+      LoadF32<F32, 4>::run(row + w.p0 / 2, c);
+      LoadF32<F32, 4>::run(row + half + w.p0 / 2, s);
+    }
+    if (w.t1) {
+      LoadF32<F32, 4>::run(row + w.p1 / 2, c + 4);
+      LoadF32<F32, 4>::run(row + half + w.p1 / 2, s + 4);
+    }
+  } else if (w.t0) {
+    LoadF32<F32, 8>::run(row + w.p0, c);
+    LoadF32<F32, 8>::run(row + half + w.p0, s);
+  }
+}
+
+// x and y (the unit's two groups) as fp32, rotated.
 __device__ __forceinline__ void rotate(float (&x)[8], float (&y)[8], const float (&c)[8],
-                                       const float (&s)[8], bool interleaved) {
+                                       const float (&s)[8], bool interleaved, const UnitPlace& w) {
   auto turn = [](float& p, float& q, float cs, float sn) {
     const float a = __fsub_rn(__fmul_rn(p, cs), __fmul_rn(q, sn));
     const float b = __fadd_rn(__fmul_rn(p, sn), __fmul_rn(q, cs));
@@ -116,27 +165,13 @@ __device__ __forceinline__ void rotate(float (&x)[8], float (&y)[8], const float
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
-      turn(y[2 * i], y[2 * i + 1], c[4 + i], s[4 + i]);
+      if (w.t0) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+      if (w.t1) turn(y[2 * i], y[2 * i + 1], c[4 + i], s[4 + i]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i]);
   }
-}
-
-// Elements (of head_dim) where unit u's two groups of 8 start.
-__device__ __forceinline__ void unit_places(int u, int rotary, bool interleaved, int* p0, int* p1) {
-  const bool half = !interleaved && u < rotary / 16;
-  *p0 = half ? 8 * u : 16 * u;
-  *p1 = half ? rotary / 2 + 8 * u : 16 * u + 8;
-}
-
-__device__ __forceinline__ void load_angles(const AppendArgs& a, int pos, int u, float (&c)[8],
-                                            float (&s)[8]) {
-  const float* row = a.angles + static_cast<size_t>(pos) * a.rotary + 8 * u;
-  LoadF32<F32, 8>::run(row, c);
-  LoadF32<F32, 8>::run(row + a.rotary / 2, s);
 }
 
 // 8 fp32 values to the destination type (times inv for E4M3), rounded once.
@@ -203,9 +238,9 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int cta) {
     return;
   }
   const int pos = c.first + in_chunk;
-  const bool turned = u < a.rotary / 16;
-  int p0, p1;
-  unit_places(u, a.rotary, a.interleaved != 0, &p0, &p1);
+  const UnitPlace w = unit_place(u, D, a.rotary, a.interleaved != 0);
+  const int p0 = w.p0, p1 = w.p1;
+  const bool turned = w.t0 || w.t1;
   int blk = -1;
   if (!BS && row_end > a.n_q) {
     blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + pos / a.block_size];
@@ -215,7 +250,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int cta) {
     }
   }
   float cs[8], sn[8];
-  if (turned) load_angles(a, pos, u, cs, sn);
+  if (turned) load_angles(a, angle_row(a, pos), w, cs, sn);
   for (int r0 = row_first; r0 < row_end; r0 += kU) {
     Raw8<Src> x[kU], y[kU];
 #pragma unroll
@@ -256,7 +291,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int cta) {
         float fx[8], fy[8];
         LoadF32<Src, 8>::run(&x[k], fx);
         LoadF32<Src, 8>::run(&y[k], fy);
-        rotate(fx, fy, cs, sn, a.interleaved != 0);
+        rotate(fx, fy, cs, sn, a.interleaved != 0, w);
         if (is_q) {
           store_f8<Src>(fx, a.q_out, dst + p0, 1.f);
           store_f8<Src>(fy, a.q_out, dst + p1, 1.f);
@@ -285,90 +320,182 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// One warp: the chunk's tokens of one (touched block, KV head, K|V).  Lanes
-// take 16 elements of a row each, 4 rows (head_dim 128) or 8 rows at a time.
+// The scale of a block after new rows of maximum m (S_before 0 where the block
+// holds nothing or its scale is no number).
+__device__ __forceinline__ float grown_scale(float before, float m) { return fmaxf(before, scale_for(m)); }
+__device__ __forceinline__ float valid_scale(float s) { return s > 0.f && s <= 1099511627776.f ? s : 0.f; }   // 2^40
+
+// max(m, |x|) over finite x: an infinity saturates, a NaN stays, neither sets
+// the scale.
+__device__ __forceinline__ float amax8(const float (&x)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = fabsf(x[i]);
+    m = v <= 3.402823466e38f ? fmaxf(m, v) : m;
+  }
+  return m;
+}
+
+// Earlier rows [0, r0) of a block whose scale grew, rounded again; lanes `lane`
+// of `lanes`, a 16-byte piece each.
+template <int D>
+__device__ __forceinline__ void requantise(uint8_t* base, int r0, float ratio, int lane, int lanes) {
+  for (int i = lane; i < r0 * (D / 16); i += lanes) {
+    uint8_t* p = base + 16 * static_cast<size_t>(i);
+    float x[8], y[8];
+    LoadF32<E4M3, 8>::run(p, x);
+    LoadF32<E4M3, 8>::run(p + 8, y);
+    store_f8<E4M3>(x, p, 0, ratio);
+    store_f8<E4M3>(y, p, 8, ratio);
+  }
+}
+
+// One new token: the D / 16 lanes of a (sequence, KV head, K|V) hold its row.
 template <typename Src, int D>
-__device__ __forceinline__ void append_block(const AppendArgs& a, int seq, int j, int h, int which) {
+__device__ __forceinline__ void append_token(const AppendArgs& a, int seq, int h, int which) {
   constexpr int kUnits = D / 16;
-  constexpr int kRows = 32 / kUnits;   // rows per pass
   constexpr unsigned FULL = 0xffffffffu;
-  const int lane = threadIdx.x & 31, u = lane % kUnits, sub = lane / kUnits;
+  const int u = threadIdx.x % kUnits;
   const int T = a.block_size;
+  const bool in = seq < a.num_seqs;
+  const Chunk c = in ? chunk_of(a, seq) : Chunk{0, 0, -1, false};
+  const bool good = in && !c.bad && c.first >= 0;
+  if (in && c.bad && u == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
+  const UnitPlace w = unit_place(u, D, a.rotary, a.interleaved != 0);
+  float x[8], y[8], m = 0.f;
+  int blk = -1;
+  if (good) {   // the row and its angles beside the table entry
+    blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + c.first / T];
+    const typename Src::raw* p = static_cast<const typename Src::raw*>(a.src[which]) +
+                                 static_cast<size_t>(c.row0) * a.src_stride[which] + static_cast<size_t>(h) * D;
+    LoadF32<Src, 8>::run(p + w.p0, x);
+    LoadF32<Src, 8>::run(p + w.p1, y);
+    if (which == 0 && (w.t0 || w.t1)) {
+      float cs[8], sn[8];
+      load_angles(a, angle_row(a, c.first), w, cs, sn);
+      rotate(x, y, cs, sn, a.interleaved != 0, w);
+    }
+    m = amax8(y, amax8(x, m));
+  }
+#pragma unroll
+  for (int o = kUnits / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+  if (!good) return;
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (u == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_TABLE);
+    return;
+  }
+  const int row = c.first % T;
+  const size_t slab = static_cast<size_t>(blk) * a.n_kv + h;
+  float* scale_at = a.block_scales + slab * 2 + which;
+  const float before = row > 0 ? valid_scale(*scale_at) : 0.f;
+  const float scale = grown_scale(before, m), inv = __frcp_rn(scale);
+  uint8_t* base = static_cast<uint8_t*>(a.cache[which]) + slab * T * D;
+  store_f8<E4M3>(x, base, static_cast<size_t>(row) * D + w.p0, inv);
+  store_f8<E4M3>(y, base, static_cast<size_t>(row) * D + w.p1, inv);
+  if (scale > before) {
+    if (row > 0) requantise<D>(base, row, __fdiv_rn(before, scale), u, kUnits);
+    // every lane of the row has read the old scale
+    __syncwarp(__activemask());
+    if (u == 0) *scale_at = scale;
+  }
+}
+
+// Chunks: 16 rows of one (touched block, KV head, K|V) per warp, kept as they
+// came in registers between the maximum and the rounding; a block of 32 is two
+// warps', which share their maximum (named barrier, both come by).  A CTA's
+// warps are of one block, K heads before V heads, and share the angles of its
+// rows in shared memory: read per head, they were as many bytes as the rows.
+template <typename Src, int D>
+__device__ __forceinline__ void append_block(const AppendArgs& a, int seq, int j, int part, float* s_angles,
+                                             float* s_max) {
+  constexpr int kUnits = D / 16;
+  constexpr int kRows = 32 / kUnits;      // rows per pass
+  constexpr int kPasses = 16 / kRows;
+  constexpr unsigned FULL = 0xffffffffu;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % kUnits, sub = lane / kUnits;
+  const int T = a.block_size, warps = T / 16;
   const Chunk c = chunk_of(a, seq);
-  if (c.n == 0 || c.first < 0) return;
+  if (c.n == 0) return;
   if (c.bad) {
-    if (lane == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
+    if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
     return;
   }
   const int lb = c.first / T + j;
   const int end = c.first + c.n;
   if (lb * T >= end) return;
   const int r0 = max(c.first - lb * T, 0), r1 = min(end - lb * T, T);   // the new rows
-  const int blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + lb];
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (lane == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_TABLE);
-    return;
-  }
-  float* scale_at = a.block_scales + (static_cast<size_t>(blk) * a.n_kv + h) * 2 + which;
-  float before = 0.f;
-  if (r0 > 0) {
-    before = *scale_at;
-    if (!(before > 0.f && before <= 1099511627776.f)) before = 0.f;   // 2^40
-  }
-  int p0, p1;
-  unit_places(u, a.rotary, a.interleaved != 0, &p0, &p1);
-  const bool turned = which == 0 && u < a.rotary / 16;
-  auto load = [&](int row, float (&x)[8], float (&y)[8]) {
+  const int unit = (part * (kThreads / 32) + warp) / warps, half = warp % warps;
+  const int which = unit >= a.n_kv, h = unit - which * a.n_kv;
+  const bool mine = unit < 2 * a.n_kv;
+  const UnitPlace w = unit_place(u, D, a.rotary, a.interleaved != 0);
+  const bool turned = which == 0 && (w.t0 || w.t1);
+  // the rows, the table entry and the angles are all on their way at once
+  Raw8<Src> xr[kPasses], yr[kPasses];
+  float m = 0.f;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int row = 16 * half + kRows * p + sub;
+    if (!mine || row < r0 || row >= r1) continue;
     const size_t tok = static_cast<size_t>(c.row0) + (lb * T + row - c.first);
-    const typename Src::raw* p = static_cast<const typename Src::raw*>(a.src[which]) +
-                                 tok * a.src_stride[which] + static_cast<size_t>(h) * D;
-    LoadF32<Src, 8>::run(p + p0, x);
-    LoadF32<Src, 8>::run(p + p1, y);
+    const size_t at = tok * a.src_stride[which] + static_cast<size_t>(h) * D;
+    xr[p] = load_raw8<Src>(a.src[which], at + w.p0);
+    yr[p] = load_raw8<Src>(a.src[which], at + w.p1);
+  }
+  const int blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + lb];
+  if (a.rotary > 0 && part * (kThreads / 32) / warps < a.n_kv) {   // a K head among them
+    const float4* src = reinterpret_cast<const float4*>(angle_row(a, lb * T + r0));
+    float4* dst = reinterpret_cast<float4*>(s_angles + r0 * a.rotary);
+    for (int i = threadIdx.x; i < (r1 - r0) * a.rotary / 4; i += kThreads) dst[i] = src[i];
+  }
+  __syncthreads();
+  if (!mine) return;
+  // the rotated values of pass p, computed for the maximum and again for the
+  // rounding: kept, they would take twice the registers and half the warps
+  auto values = [&](int p, float (&x)[8], float (&y)[8]) {
+    LoadF32<Src, 8>::run(&xr[p], x);
+    LoadF32<Src, 8>::run(&yr[p], y);
     if (turned) {
       float cs[8], sn[8];
-      load_angles(a, lb * T + row, u, cs, sn);
-      rotate(x, y, cs, sn, a.interleaved != 0);
+      load_angles(a, s_angles + (16 * half + kRows * p + sub) * a.rotary, w, cs, sn);
+      rotate(x, y, cs, sn, a.interleaved != 0, w);
     }
   };
-  // non-finite values do not set the scale: an infinity saturates, a NaN stays
-  auto amax = [](const float (&x)[8], float m) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = fabsf(x[i]);
-      m = v <= 3.402823466e38f ? fmaxf(m, v) : m;
-    }
-    return m;
-  };
-  float m = 0.f;
-  for (int row = r0 + sub; row < r1; row += kRows) {
+  for (int p = 0; p < kPasses; ++p) {
+    const int row = 16 * half + kRows * p + sub;
+    if (row < r0 || row >= r1) continue;
     float x[8], y[8];
-    load(row, x, y);
-    m = amax(y, amax(x, m));
+    values(p, x, y);
+    m = amax8(y, amax8(x, m));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-  const float scale = fmaxf(before, scale_for(m));
-  const float inv = __frcp_rn(scale);
-  uint8_t* base = static_cast<uint8_t*>(a.cache[which]) +
-                  (static_cast<size_t>(blk) * a.n_kv + h) * T * D;
-  for (int row = r0 + sub; row < r1; row += kRows) {
+  if (blk < 0 || blk >= a.num_blocks) {   // the same for both warps of a block
+    if (lane == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_TABLE);
+    return;
+  }
+  const size_t slab = static_cast<size_t>(blk) * a.n_kv + h;
+  float* scale_at = a.block_scales + slab * 2 + which;
+  const float before = r0 > 0 ? valid_scale(*scale_at) : 0.f;
+  if (T > 16) {
+    if (lane == 0) s_max[warp] = m;
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");   // both have read the scale too
+    m = fmaxf(m, s_max[warp ^ 1]);
+  }
+  const float scale = grown_scale(before, m), inv = __frcp_rn(scale);
+  uint8_t* base = static_cast<uint8_t*>(a.cache[which]) + slab * T * D;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int row = 16 * half + kRows * p + sub;
+    if (row < r0 || row >= r1) continue;
     float x[8], y[8];
-    load(row, x, y);
-    store_f8<E4M3>(x, base, static_cast<size_t>(row) * D + p0, inv);
-    store_f8<E4M3>(y, base, static_cast<size_t>(row) * D + p1, inv);
+    values(p, x, y);
+    store_f8<E4M3>(x, base, static_cast<size_t>(row) * D + w.p0, inv);
+    store_f8<E4M3>(y, base, static_cast<size_t>(row) * D + w.p1, inv);
   }
-  if (scale > before && r0 > 0) {   // the earlier rows at the new scale
-    const float ratio = __fdiv_rn(before, scale);
-    for (int row = sub; row < r0; row += kRows) {
-      uint8_t* p = base + static_cast<size_t>(row) * D + 16 * u;
-      float x[8], y[8];
-      LoadF32<E4M3, 8>::run(p, x);
-      LoadF32<E4M3, 8>::run(p + 8, y);
-      store_f8<E4M3>(x, p, 0, ratio);
-      store_f8<E4M3>(y, p, 8, ratio);
-    }
-  }
-  if (lane == 0) *scale_at = scale;
+  if (scale > before && r0 > 0)
+    requantise<D>(base, r0, __fdiv_rn(before, scale), lane + 32 * half, 32 * warps);
+  if (lane == 0 && half == 0) *scale_at = scale;
 }
 
 template <typename Src, typename Dst, int D, bool BS>
@@ -381,12 +508,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   if (!BS || cta < a.row_ctas) {
     append_rows<Src, Dst, D, BS>(a, cta);
   } else {
-    const int w = (cta - a.row_ctas) * (kThreads / 32) + threadIdx.x / 32;
-    const int per = 2 * a.n_kv;
-    const int i = w / per, hw = w - i * per;
-    const int seq = a.query_start == nullptr ? i : blockIdx.z;
-    const int j = a.query_start == nullptr ? 0 : i;
-    if (seq < a.num_seqs) append_block<Src, D>(a, seq, j, hw >> 1, hw & 1);
+    if (a.query_start == nullptr) {
+      const int per = 2 * a.n_kv;
+      const int i = (cta - a.row_ctas) * (kThreads * 16 / D) + threadIdx.x / (D / 16);
+      const int seq = i / per, hw = i - seq * per;
+      append_token<Src, D>(a, seq, hw >> 1, hw & 1);
+    } else {
+      __shared__ __align__(16) float s_angles[32 * D];   // up to 32 rows of up to head_dim
+      __shared__ float s_max[kThreads / 32];
+      const int i = cta - a.row_ctas;
+      append_block<Src, D>(a, blockIdx.z, i / a.block_parts, i % a.block_parts, s_angles, s_max);
+    }
   }
 }
 
@@ -399,30 +531,42 @@ pkv_status launch_append(AppendArgs a, cudaStream_t st) {
   // a decode step has few tokens: one batch of loads per thread, the rows
   // spread over more CTAs; many tokens fill the GPU with whole tokens
   const int64_t tokens = one ? a.num_seqs : a.total;
-  a.rows_per_cta = tokens >= 4096 ? 12 : 4;
-  a.row_groups = rows > 0 ? (rows + a.rows_per_cta - 1) / a.rows_per_cta : 1;
+  // (rows per CTA of 12 and 36: 6,400 tokens of 36 rows 24.3 and 28.0 us,
+  // 40,000 of 64 rows 282 and 264 us)
+  const int most = tokens >= 16384 ? 36 : tokens >= 4096 ? 12 : 4;
+  a.row_groups = rows > 0 ? (rows + most - 1) / most : 1;
+  a.rows_per_cta = std::max((rows + a.row_groups - 1) / a.row_groups, 1);
   const int64_t row_ctas = rows > 0 ? tiles * a.row_groups : 0;
-  int64_t block_warps = 0;
+  int64_t block_ctas = 0;
   if (BS) {
-    const int64_t touched = one ? a.num_seqs : (a.max_len + a.block_size - 2) / a.block_size + 1;
-    block_warps = touched * 2 * a.n_kv;
+    constexpr int kWarps = kThreads / 32;
+    if (one) {
+      block_ctas = (static_cast<int64_t>(a.num_seqs) * 2 * a.n_kv * (D / 16) + kThreads - 1) / kThreads;
+    } else {
+      a.block_parts = (2 * a.n_kv * (a.block_size / 16) + kWarps - 1) / kWarps;
+      const int64_t touched = (a.max_len + static_cast<int64_t>(a.block_size) - 2) / a.block_size + 1;
+      block_ctas = touched * a.block_parts;
+    }
   }
-  const int64_t ctas = row_ctas + (block_warps + kThreads / 32 - 1) / (kThreads / 32);
-  if (ctas > INT32_MAX || block_warps > INT32_MAX)
+  const int64_t ctas = row_ctas + block_ctas;
+  if (ctas > INT32_MAX)
     return fail(PKV_ERR_UNSUPPORTED, "pkv_append: too many tokens in one call");
   if (ctas == 0) return PKV_OK;
   a.row_ctas = static_cast<int32_t>(row_ctas);
-  static std::atomic<uint64_t> carveout{0};
-  prefer_max_shared(append_kernel<Src, Dst, D, BS>, carveout);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, one ? 1 : a.num_seqs);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // between a decode step's attention kernels the SMs keep their split of L1
+  // and shared memory; many tokens want their angles in L1 (6,400 tokens: 24.3
+  // us, 29.6 with the least L1)
+  attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+  attr[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = tokens < 4096 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, append_kernel<Src, Dst, D, BS>, a);
   if (e != cudaSuccess) return cuda_fail("pkv_append: launch", e);
   return check_launch("pkv_append");

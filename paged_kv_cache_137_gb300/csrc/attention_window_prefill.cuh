@@ -521,9 +521,14 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     // ---------------------------------------------------------- MMA issuers
     // one warp a tile: its waits do not hold up the other tile's MMAs
     const int X = warp - kMmaWarp;
-    // no vote: nothing below needs the lanes together (an instruction is its
-    // leader's), and the votes added up in this warp's chain
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(smem_u32(bar), parity, kWaitNs); };
+    // No vote in a wait: an instruction is its leader's, and votes added up in
+    // this warp's chain.  A lane whose wait gives up goes on without waiting to
+    // the end of the unit, where the lanes agree to stop (what it issues until
+    // then stays within the CTA's shared memory and TMEM).
+    bool late = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!late) late = !mbar_wait(smem_u32(bar), parity, kWaitNs);
+    };
     const uint32_t leader = elect_one();
     const uint32_t tm = __reduce_max_sync(FULL, tmem) + 256 * X;   // uniform for the compiler as well
     const uint64_t q_desc = sw128_desc(smem_u32(q_s + X * S_::kQTile), 16, 1024);
@@ -533,16 +538,18 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     RingPos<kBufV> vp;   // of the next P V
     RingPos<2> sq, sp;   // S / P buffers of the next Q K^T and the next P V
     int units = 0;       // of this tile so far
-    bool ok = true;
     Work w;
-    for (int k = 0; ok && next_work(k, w); ++k) {
+    for (int k = 0; next_work(k, w); ++k) {
       const int nt = X ? w.nt[1] : w.nt[0], steps = w.steps;
+      // steps [inner0, inner1) have no V row that nobody sees
+      const int inner0 = (w.keys.ns + (w.keys.wb * kChunkKeys < w.keys.w0) + kStepChunks - 1) / kStepChunks;
+      const int inner1 = (w.keys.ns + max((w.keys.last + 1) / kChunkKeys - w.keys.wb, 0)) / kStepChunks;
       release_work(k);
-      auto qk = [&](bool last) -> bool {
+      auto qk = [&](bool last) {
         const int i = 2 * X + sq.slot;
-        if (!wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par)) return false;
+        wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par);
         // the buffer's step before: its P has been read by P V
-        if (sq.used && !wait(&o_done[i], sq.par ^ 1)) return false;
+        if (sq.used) wait(&o_done[i], sq.par ^ 1);
         tc_fence_after();
         const uint64_t kd = k_desc + static_cast<uint32_t>(kp.slot * (S_::kStrideK >> 4));
         const uint32_t d_tmem = tm + 64 * sq.slot;
@@ -555,41 +562,68 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         if (last) commit(leader, smem_u32(&q_free[X]));
         kp.next();
         sq.next();
-        return true;
       };
-      auto pv = [&](bool first) -> bool {
+      auto pv = [&](int t) {
         const int i = 2 * X + sp.slot;
+        // V rows that nobody sees (16-bit caches; the helpers leave zeros), while
+        // P is made: both tiles write the same zeros, each before its own P V
+        if constexpr (!kFp8) {
+          if (t < inner0 || t >= inner1) {
+            constexpr int kPieces = 8 * S_::kSlabs;   // 16-byte pieces of a row, a lane each
+            uint8_t* vt = ring + vp.slot * S_::kStage + S_::kTile + (lane % kPieces >> 3) * kSlab + (lane & 7) * 16;
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = w.keys.chunk(kStepChunks * t + 2 * h + (lane >> 4));
+              const uint32_t none = __ballot_sync(FULL, !w.keys.any_sees(c * kChunkKeys + (lane & 15)));
+              if (none != 0)
+                for (int r = lane / kPieces; r < 32; r += 32 / kPieces)
+                  if (none >> r & 1u)
+                    *reinterpret_cast<uint4*>(vt + (32 * h + r) * 128) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();   // before the tensor core reads V
+            __syncwarp();
+          }
+        }
         // O of the unit before has been read
-        if (first && units > 0 && !wait(&o_free[X], (units - 1) & 1)) return false;
-        if (!wait(&p_full[i], sp.par)) return false;
+        if (t == 0 && units > 0) wait(&o_free[X], (units - 1) & 1);
+        wait(&p_full[i], sp.par);
         tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>(vp.slot * (S_::kStrideV >> 4));
         const uint32_t p_tmem = tm + 64 * sp.slot;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(leader, tm + 128, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
+          mma_ts(leader, tm + 128, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (t > 0 || kk > 0) ? 1u : 0u);
         commit(leader, smem_u32(&o_done[i]));
         commit(leader, smem_u32(kFp8 ? &v_free[vp.slot] : &empty[vp.slot]));
         vp.next();
         sp.next();
-        return true;
       };
       if (nt > 0) {
-        ok = wait(&q_full[X], units & 1) && qk(nt == 1) && (nt < 2 || qk(nt == 2));
-        for (int t = 0; t < nt && ok; ++t) ok = pv(t == 0) && (t + 2 >= nt || qk(t + 3 == nt));
+        wait(&q_full[X], units & 1);
+        qk(nt == 1);
+        if (nt > 1) qk(nt == 2);
+        for (int t = 0; t < nt; ++t) {
+          pv(t);
+          if (t + 2 < nt) qk(t + 3 == nt);
+        }
         ++units;
       }
       // the stream's steps that only the other tile reads
-      for (int t = nt; t < steps && ok; ++t) {
-        ok = wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par) && (!kFp8 || wait(&v_full[vp.slot], vp.par));
-        if (ok && lane == 0) {
+      for (int t = nt; t < steps; ++t) {
+        wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par);
+        if (kFp8) wait(&v_full[vp.slot], vp.par);
+        if (lane == 0) {
           if (kFp8) mbar_arrive(smem_u32(&k_free[kp.slot]));
           mbar_arrive(smem_u32(kFp8 ? &v_free[vp.slot] : &empty[vp.slot]));
         }
         kp.next();
         vp.next();
       }
-      if (!ok) give_up();
+      if (__any_sync(FULL, late)) {
+        give_up();
+        break;
+      }
     }
     commit(leader, smem_u32(&fin));
   } else if (warp >= kHelpWarp) {
@@ -819,7 +853,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tX = tmem + 256 * X + lane_off, tO = tX + 128;
     RingPos<2> sp;             // S / P buffer
-    RingPos<kRing> at;         // stage of the stream
     RingPos<kWideV> av;        // widened V buffer
     int g = 0, units = 0;      // stream steps and this tile's units so far
     bool ok = true;
@@ -935,30 +968,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         tmem_st32u(tX + 64 * b, pw);
         const float2 sum = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
         l = fmaf(sum.x + sum.y, inv_v, l);
-        // V rows that nobody sees (16-bit caches; the helpers leave zeros);
-        // both tiles' threads write them, each before its own P V
-        if constexpr (!kFp8) {
-          if (!u.keys.inner(t) && r < kKeys) {
-            const int p = u.keys.chunk(kStepChunks * t + (r >> 4)) * kChunkKeys + (r & 15);
-            if (!u.keys.any_sees(p)) {
-              uint8_t* vt = ring + at.slot * S_::kStage + S_::kTile + r * 128;
-#pragma unroll
-              for (int e = 0; e < 8 * S_::kSlabs; ++e)
-                *reinterpret_cast<uint4*>(vt + (e >> 3) * kSlab + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async();   // before the tensor core reads V
-            }
-          }
-        }
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[i]));
         sp.next();
-        at.next();
         if (kFp8) av.next();
       }
-      for (int t = ntx; t < u.steps; ++t) {   // the stream's steps of the other tile
-        at.next();
-        if (kFp8) av.next();
-      }
+      if (kFp8)
+        for (int t = ntx; t < u.steps; ++t) av.next();   // the stream's steps of the other tile
       if (ok && ntx > 0) {
         // the row's factor for the helpers, who are done with the unit before
         ok = units == 0 || wait(&o_free[X], (units - 1) & 1);

@@ -230,7 +230,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int cta) {
     if (c.bad && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
     // (a chunk longer than max_len has more rows than the grid has tokens)
     const float fill = c.bad ? CUDART_NAN_F : 0.f;
-    const int64_t step = static_cast<int64_t>((a.max_len + kTok - 1) / kTok) * kTok;
+    const int64_t step = (static_cast<int64_t>(a.max_len) + kTok - 1) / kTok * kTok;
     for (int64_t i = in_chunk; i < c.n; i += step)
       for (int r = row_first; r < min(row_end, a.n_q); ++r)
         for (int e = 0; e < 16; ++e)
@@ -422,7 +422,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int seq, int j
   }
   const int lb = c.first / T + j;
   const int end = c.first + c.n;
-  if (lb * T >= end) return;
+  if (static_cast<int64_t>(lb) * T >= end) return;
   const int r0 = max(c.first - lb * T, 0), r1 = min(end - lb * T, T);   // the new rows
   const int unit = (part * (kThreads / 32) + warp) / warps, half = warp % warps;
   const int which = unit >= a.n_kv, h = unit - which * a.n_kv;
@@ -527,7 +527,7 @@ pkv_status launch_append(AppendArgs a, cudaStream_t st) {
   constexpr int kTok = kThreads / (D / 16);
   const int rows = a.n_q + (BS ? 0 : 2 * a.n_kv);
   const bool one = a.query_start == nullptr;
-  const int64_t tiles = one ? (a.num_seqs + kTok - 1) / kTok : (a.max_len + kTok - 1) / kTok;
+  const int64_t tiles = (static_cast<int64_t>(one ? a.num_seqs : a.max_len) + kTok - 1) / kTok;
   // a decode step has few tokens: one batch of loads per thread, the rows
   // spread over more CTAs; many tokens fill the GPU with whole tokens
   const int64_t tokens = one ? a.num_seqs : a.total;
@@ -694,7 +694,8 @@ extern "C" pkv_status pkv_append(void* k_cache, void* v_cache, float* block_scal
   a.max_blocks = max_blocks;
   a.num_seqs = num_seqs;
   a.total = total_tokens;
-  a.max_len = max_query_len;
+  // no chunk that is written is longer than the inputs or than a context
+  a.max_len = std::min({max_query_len, total_tokens, max_blocks * desc->block_size});
   a.n_q = num_q_heads;
   a.n_kv = desc->num_kv_heads;
   a.block_size = desc->block_size;

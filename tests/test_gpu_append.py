@@ -261,6 +261,20 @@ def test_invalid_lengths_and_tables_write_nothing_of_theirs(kv):
     assert torch.isnan(e.q_out[3:].float()).all() and not torch.isnan(e.q_out[:3].float()).any()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_the_largest_longest_chunk(kv):
+    """max_query_len bounds the chunks from above: any larger value, the largest
+    of its type as well, gives the same call."""
+    a, b = (Batch(CTX, [1, 3, 16, 5, 0, 32, 20, 64, 7], kv=kv, seed=8) for _ in range(2))
+    sa, sb = ((torch.ones((x.nb, x.hkv, 2), device="cuda") if kv == "e4m3" else None) for x in (a, b))
+    a.call(block_scales=sa)
+    b.call(block_scales=sb, max_query_len=2 ** 31 - 1)
+    assert pkv.pkv_device_status() == 0
+    assert torch.equal(a.q_out, b.q_out) and (sa is None or torch.equal(sa, sb))
+    assert torch.equal(a.k_cache.view(torch.uint8), b.k_cache.view(torch.uint8))
+    assert torch.equal(a.v_cache.view(torch.uint8), b.v_cache.view(torch.uint8))
+
+
 def test_rows_outside_the_chunks_are_left_alone():
     """Rows before the first chunk and behind the last, an empty chunk, and an
     empty sequence of a one-token call."""

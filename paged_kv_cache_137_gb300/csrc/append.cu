@@ -362,10 +362,17 @@ __device__ __forceinline__ void append_token(const AppendArgs& a, int seq, int h
   const bool good = in && !c.bad && c.first >= 0;
   if (in && c.bad && u == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
   const UnitPlace w = unit_place(u, D, a.rotary, a.interleaved != 0);
-  float x[8], y[8], m = 0.f;
-  int blk = -1;
-  if (good) {   // the row and its angles beside the table entry
-    blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + c.first / T];
+  float x[8], y[8], m = 0.f, before = 0.f;
+  const int row = good ? c.first % T : 0;
+  float* scale_at = nullptr;   // NULL: a bad table entry
+  size_t slab = 0;
+  if (good) {   // the row and its angles beside the table entry and the scale
+    const int blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + c.first / T];
+    if (blk >= 0 && blk < a.num_blocks) {
+      slab = static_cast<size_t>(blk) * a.n_kv + h;
+      scale_at = a.block_scales + slab * 2 + which;
+      if (row > 0) before = valid_scale(*scale_at);
+    }
     const typename Src::raw* p = static_cast<const typename Src::raw*>(a.src[which]) +
                                  static_cast<size_t>(c.row0) * a.src_stride[which] + static_cast<size_t>(h) * D;
     LoadF32<Src, 8>::run(p + w.p0, x);
@@ -379,23 +386,18 @@ __device__ __forceinline__ void append_token(const AppendArgs& a, int seq, int h
   }
 #pragma unroll
   for (int o = kUnits / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+  __syncwarp();   // every lane of a row has read the old scale
   if (!good) return;
-  if (blk < 0 || blk >= a.num_blocks) {
+  if (scale_at == nullptr) {
     if (u == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_TABLE);
     return;
   }
-  const int row = c.first % T;
-  const size_t slab = static_cast<size_t>(blk) * a.n_kv + h;
-  float* scale_at = a.block_scales + slab * 2 + which;
-  const float before = row > 0 ? valid_scale(*scale_at) : 0.f;
   const float scale = grown_scale(before, m), inv = __frcp_rn(scale);
   uint8_t* base = static_cast<uint8_t*>(a.cache[which]) + slab * T * D;
   store_f8<E4M3>(x, base, static_cast<size_t>(row) * D + w.p0, inv);
   store_f8<E4M3>(y, base, static_cast<size_t>(row) * D + w.p1, inv);
   if (scale > before) {
     if (row > 0) requantise<D>(base, row, __fdiv_rn(before, scale), u, kUnits);
-    // every lane of the row has read the old scale
-    __syncwarp(__activemask());
     if (u == 0) *scale_at = scale;
   }
 }
@@ -481,6 +483,8 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int seq, int j
     if (lane == 0) s_max[warp] = m;
     asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");   // both have read the scale too
     m = fmaxf(m, s_max[warp ^ 1]);
+  } else {
+    __syncwarp();   // every lane has read it
   }
   const float scale = grown_scale(before, m), inv = __frcp_rn(scale);
   uint8_t* base = static_cast<uint8_t*>(a.cache[which]) + slab * T * D;

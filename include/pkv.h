@@ -591,8 +591,9 @@ PKV_API pkv_status pkv_copy_block_scales(float* const* block_scales, int32_t num
  * Table entries of blocks that no query of the call sees are not read, so
  * those blocks may have gone back to the pool.  The block-scaled calls read
  * an E4M3 cache as e4m3 * block_scales[block][KV head][K|V] (as pkv_append
- * writes it; scales from 2^-40 to 2^40); with them window_tokens 0 means the
- * whole context.  sink_tokens is ignored where nothing else is hidden. */
+ * writes it; a scale outside 2^-40 .. 2^40 counts as the nearer end, NaN as
+ * 2^-40); with them window_tokens 0 means the whole context.  sink_tokens is
+ * ignored where nothing else is hidden. */
 
 /* Workspace bytes of the windowed and block-scaled decode calls for these
  * sizes (0 if no split is needed). */
@@ -625,7 +626,8 @@ PKV_API pkv_status pkv_attention_decode_block_scaled(
  * 1; each query by its own position): arguments, layout, launch and errors as
  * there.  Runs on tcgen05 for every cache it takes, 16-bit with head_dim 64 or
  * 128 and E4M3 with head_dim 128, whatever the sign of softmax_scale;
- * pkv_set_prefill_kernel does not apply.  A NaN or an infinity in V at a
+ * pkv_set_prefill_kernel does not apply.  At most 1024 query heads per KV head
+ * and 2^31 - 1 query rows (total_q * that) in a call.  A NaN or an infinity in V at a
  * position that one query of the call sees can reach the others of its KV
  * head's 256 rows (a weight of 0 times it is NaN), as in pkv_attention_prefill. */
 PKV_API pkv_status pkv_attention_prefill_window(

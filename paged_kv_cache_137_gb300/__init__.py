@@ -855,8 +855,10 @@ def _append_args(k_cache, v_cache, k, v, block_tables, context_lens, desc, query
         op = _on(q_out, "q_out", dtype, (n, hq, d), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if rope is not None and rope._cos_sin.get_device() != dev:
-        raise ValueError("the rotation's table must be on the current CUDA device")
+    if rope is not None:  # (a pkv_rope filled by hand holds no tensor)
+        table = getattr(rope, "_cos_sin", None)
+        if table is not None and table.get_device() != dev:
+            raise ValueError("the rotation's table must be on the current CUDA device")
     return (kc, vc, None if block_scales is None else _scales(block_scales, desc, dev), kp, ks, vp, vs, op, qp, qs,
             hq, _dtype_code(k), tp, m, cp, sp, b, n, longest, None if rope is None else ctypes.byref(rope),
             ctypes.byref(desc), k_inv_scale, v_inv_scale)

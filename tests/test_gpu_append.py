@@ -321,6 +321,34 @@ def test_prepared_captured_and_on_another_stream(kv):
     assert sa is None or torch.equal(sa, sb)
 
 
+def test_a_rope_filled_by_hand():
+    a, b = (Batch(CTX, [1] * len(CTX), seed=9) for _ in range(2))
+    b.rope = pkv.pkv_rope(b.table.data_ptr(), b.table.shape[0], b.table.shape[1], 0)
+    a.call(one=True)
+    b.call(one=True)
+    assert torch.equal(a.q_out, b.q_out) and torch.equal(a.k_cache, b.k_cache)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each on blocks of its own, give what they give one
+    after the other."""
+    a, b = (Batch(CTX, [1, 3, 16, 5, 0, 32, 20, 64, 7], kv="e4m3", seed=s) for s in (10, 11))
+    both = [Batch(CTX, [1, 3, 16, 5, 0, 32, 20, 64, 7], kv="e4m3", seed=s) for s in (10, 11)]
+    scales = [torch.full((x.nb, x.hkv, 2), 2.0 ** -9, device="cuda") for x in (a, b, *both)]
+    a.call(block_scales=scales[0])
+    b.call(block_scales=scales[1])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for x, sc, st in zip(both, scales[2:], streams):
+            st.wait_stream(torch.cuda.current_stream())
+            pkv.pkv_append(x.k_cache, x.v_cache, x.k, x.v, x.tables_d, x.ctx_d, x.desc, query_start=x.start,
+                           max_query_len=64, rope=x.rope, q=x.q, q_out=x.q_out, block_scales=sc, stream=st)
+    torch.cuda.synchronize()
+    for x, y, sx, sy in zip((a, b), both, scales[:2], scales[2:]):
+        assert torch.equal(x.q_out, y.q_out) and torch.equal(sx, sy)
+        assert torch.equal(x.k_cache, y.k_cache) and torch.equal(x.v_cache, y.v_cache)
+
+
 def test_copied_blocks_take_their_scales_along():
     desc = pkv.kv_desc(40, 3, 64, 16, "e4m3")
     layers = [torch.rand((40, 3, 2), device="cuda") for _ in range(3)]

@@ -192,3 +192,62 @@ def test_infinite_logits_and_values():
     x.check(out)
     x.v_cache[int(x.tables[0, 2]), 0, 0, 5] = float("inf")
     assert torch.isinf(attend(x)[0, :, 5]).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1)])
+def test_the_largest_windows_and_sinks(window, sinks, kernel):
+    x = Inputs(CTX, hq=4, hkv=2, kv="bf16", window=window, sinks=sinks, seed=6)
+    for part in (0, 64):
+        x.check(attend(x, part))
+
+
+def test_two_calls_at_once_and_graphs_that_share_a_workspace():
+    """Calls on two streams, each with a workspace of its own; two captured
+    calls of one workspace, replayed one after the other."""
+    xs = [Inputs([400, 900, 33], hq=8, hkv=2, kv="bf16", window=w, sinks=4, seed=w) for w in (500, 300)]
+    want = [attend(x, 64) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [pkv.window_workspace_for(3, x.hq, x.max_blocks, x.desc, x.window, 4, 64) for x in xs]
+    outs = [torch.full_like(w, float("nan")) for w in want]
+
+    def call(i, ws, stream):
+        x = xs[i]
+        pkv.pkv_attention_decode_window(outs[i], x.q_d, x.k_cache, x.v_cache, x.tables_d, x.ctx_d, x.desc, x.window,
+                                        x.sinks, x.scale, partition_tokens=64, workspace=ws, stream=stream)
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            call(i, spaces[i], streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    shared = max(spaces, key=torch.Tensor.numel)
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i, shared, None)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("scales", [None, "block"])
+def test_offsets_past_32_bits(scales, kernel):
+    """Contexts in the last blocks of a cache of more than 2^32 elements."""
+    x = Inputs([40, 33, 100], hq=8, hkv=8, kv="e4m3", scales=scales, window=60, sinks=3, seed=7)
+    want = attend(x)
+    nb = (1 << 32) // (8 * 16 * 128) + 64
+    x.desc = pkv.kv_desc(nb, 8, 128, 16, "e4m3")
+    for name in ("k_cache", "v_cache", "block_scales"):
+        small = getattr(x, name)
+        if small is not None:
+            big = torch.zeros((nb,) + small.shape[1:], dtype=small.dtype, device="cuda")
+            big[nb - x.nb:] = small
+            setattr(x, name, big)
+    x.tables_d = torch.where(x.tables_d >= 0, x.tables_d + (nb - x.nb), x.tables_d).int()
+    assert torch.equal(attend(x), want)

@@ -160,3 +160,54 @@ def test_captured_and_replayed_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1)])
+def test_the_largest_windows_sinks_and_chunk_bounds(window, sinks):
+    x = Inputs(CTX, NEW, hq=4, hkv=2, kv="bf16", window=window, sinks=sinks, seed=6)
+    x.check(attend(x, max_query_len=2 ** 31 - 1))
+    assert pkv.pkv_device_status() == 0
+
+
+@pytest.mark.parametrize("hq", [129, 300, 1024])
+def test_many_heads_of_one_kv_head(hq):
+    """A position's heads over several tiles, and over several units."""
+    x = Inputs([50, 9], [5, 2], hq=hq, hkv=1, d=64, kv="f16", q="f16", window=20, sinks=3, seed=hq)
+    x.check(attend(x))
+
+
+def test_more_heads_than_that_are_refused():
+    x = Inputs([5], [2], hq=1025, hkv=1, d=64, kv="f16", q="f16", window=20, seed=1)
+    with pytest.raises(pkv.PkvError, match="query heads per KV head"):
+        attend(x)
+
+
+def test_two_calls_at_once():
+    xs = [Inputs([400, 900, 33], [100, 300, 33], hq=8, hkv=2, kv="bf16", window=w, sinks=4, seed=w) for w in (500, 90)]
+    want = [attend(x) for x in xs]
+    outs = [torch.full_like(w, float("nan")) for w in want]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for x, out, st in zip(xs, outs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            pkv.pkv_attention_prefill_window(out, x.q_d, x.k_cache, x.v_cache, x.tables_d, x.ctx_d, x.start, x.desc,
+                                             x.window, x.sinks, x.scale, 300, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("scales", [None, "block"])
+def test_offsets_past_32_bits(scales):
+    """Contexts in the last blocks of a cache of more than 2^32 elements."""
+    x = Inputs([40, 33, 100], [40, 2, 70], hq=8, hkv=8, kv="e4m3", scales=scales, window=60, sinks=3, seed=7)
+    want = attend(x)
+    nb = (1 << 32) // (8 * 16 * 128) + 64
+    x.desc = pkv.kv_desc(nb, 8, 128, 16, "e4m3")
+    for name in ("k_cache", "v_cache", "block_scales"):
+        small = getattr(x, name)
+        if small is not None:
+            big = torch.zeros((nb,) + small.shape[1:], dtype=small.dtype, device="cuda")
+            big[nb - x.nb:] = small
+            setattr(x, name, big)
+    x.tables_d = torch.where(x.tables_d >= 0, x.tables_d + (nb - x.nb), x.tables_d).int()
+    assert torch.equal(attend(x), want)

@@ -369,10 +369,28 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 
   if (warp == kSchedWarp) {
     // ----------------------------------------------------------- scheduler
-    // Unit x of the grid is KV head x % N_kv of slot x / N_kv; sequence s has
-    // the slots from (query_start[s] * G) / 256 + s on, at least as many as
-    // its 256-row pairs, the last pair (the most keys) first.
+    // Unit x of the grid is KV head x % N_kv of slot x / N_kv; of more than 32
+    // sequences, s has the slots from (query_start[s] * G) / 256 + s on, at
+    // least as many as its 256-row pairs, the last pair (the most keys) first.
     int x = blockIdx.x, k = 0, asked = 0;
+    // Up to 32 sequences are taken longest first, lane s keeping sequence s and
+    // its first slot in that order: a long unit that starts last would leave
+    // the other SMs idle.
+    const bool few = a.num_seqs <= 32;
+    int my_q0 = 0, my_n = 0, my_ctx = 0, my_units = 0, my_slot = 0;
+    if (few) {
+      if (lane < a.num_seqs) {
+        my_q0 = a.query_start[lane];
+        my_n = a.query_start[lane + 1] - my_q0;
+        my_ctx = a.ctx_lens[lane];
+        if (my_q0 >= 0 && my_n > 0 && my_n <= a.total_q - my_q0)   // else no rows this call may write
+          my_units = static_cast<int>((static_cast<int64_t>(my_n) * G + kUnitRows - 1) / kUnitRows);
+      }
+      for (int o = 0; o < a.num_seqs; ++o) {
+        const int ctx = __shfl_sync(FULL, my_ctx, o), units = __shfl_sync(FULL, my_units, o);
+        if (ctx > my_ctx || (ctx == my_ctx && o < lane)) my_slot += units;
+      }
+    }
     while (true) {
       if (!(k < 2 || wait(&work_empty[k & 1], ((k >> 1) - 1) & 1))) {
         give_up();
@@ -400,22 +418,38 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         const int slot = x / a.num_kv_heads;
         const int kvh = x - slot * a.num_kv_heads;
         x = -1;
-        auto slot0 = [&](int s) { return static_cast<int>(static_cast<int64_t>(a.query_start[s]) * G / kUnitRows) + s; };
-        int lo = 0, hi = a.num_seqs;   // the last sequence whose slots start at or before `slot`
-        while (hi - lo > 1) {
-          const int step = (hi - lo + 31) / 32;
-          const int s = lo + lane * step;
-          const unsigned le = __ballot_sync(FULL, s < hi && slot0(s) <= slot);
-          const int c = __popc(le);
-          if (c == 0) break;
-          lo += (c - 1) * step;
-          hi = min(lo + step, hi);
+        int lo = 0, q0, n, ctx, at, pairs;
+        if (few) {
+          const unsigned here = __ballot_sync(FULL, slot >= my_slot && slot - my_slot < my_units);
+          if (here == 0) continue;   // more blocks than units
+          lo = __ffs(here) - 1;
+          q0 = __shfl_sync(FULL, my_q0, lo);
+          n = __shfl_sync(FULL, my_n, lo);
+          ctx = __shfl_sync(FULL, my_ctx, lo);
+          pairs = __shfl_sync(FULL, my_units, lo);
+          at = slot - __shfl_sync(FULL, my_slot, lo);
+        } else {
+          auto slot0 = [&](int s) {
+            return static_cast<int>(static_cast<int64_t>(a.query_start[s]) * G / kUnitRows) + s;
+          };
+          int hi = a.num_seqs;   // the last sequence whose slots start at or before `slot`
+          while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int s = lo + lane * step;
+            const unsigned le = __ballot_sync(FULL, s < hi && slot0(s) <= slot);
+            const int c = __popc(le);
+            if (c == 0) break;
+            lo += (c - 1) * step;
+            hi = min(lo + step, hi);
+          }
+          q0 = a.query_start[lo];
+          n = a.query_start[lo + 1] - q0;
+          ctx = a.ctx_lens[lo];
+          at = slot - slot0(lo);
+          if (at < 0 || q0 < 0 || n <= 0 || n > a.total_q - q0) continue;   // no rows this call may write
+          pairs = static_cast<int>((static_cast<int64_t>(n) * G + kUnitRows - 1) / kUnitRows);
+          if (at >= pairs) continue;
         }
-        const int q0 = a.query_start[lo], n = a.query_start[lo + 1] - q0, ctx = a.ctx_lens[lo];
-        const int at = slot - slot0(lo);
-        if (at < 0 || q0 < 0 || n <= 0 || n > a.total_q - q0) continue;   // no rows this call may write
-        const int pairs = static_cast<int>((static_cast<int64_t>(n) * G + kUnitRows - 1) / kUnitRows);
-        if (at >= pairs) continue;
         const int pair = pairs - 1 - at;
         if (ctx < 0 || ctx > a.max_blocks * T || n > ctx || n > a.max_q_tiles) {
           // invalid lengths: the unit's rows become NaN

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     s_timeout = s_issued = s_finished = s_claimed = 0;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), kFp8 ? 4 : 2);   // the helper warps, or both MMA warps
+      mbar_init(smem_u32(&empty[i]), kFp8 ? 4 : 1);   // the helper warps, or the P V warp
     }
     for (int i = 0; i < kWideK; ++i) {
       mbar_init(smem_u32(&k_full[i]), 2);   // the two warps that widen K
@@ -553,10 +553,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     }
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ---------------------------------------------------------- MMA issuers
-    // one warp a tile: its waits do not hold up the other tile's MMAs
-    const int X = warp - kMmaWarp;
     // No vote in a wait: an instruction is its leader's, and votes added up in
-    // this warp's chain.  A lane whose wait gives up goes on without waiting to
+    // a warp's chain.  A lane whose wait gives up goes on without waiting to
     // the end of the unit, where the lanes agree to stop (what it issues until
     // then stays within the CTA's shared memory and TMEM).
     bool late = false;
@@ -564,52 +562,139 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       if (!late) late = !mbar_wait(smem_u32(bar), parity, kWaitNs);
     };
     const uint32_t leader = elect_one();
-    const uint32_t tm = __reduce_max_sync(FULL, tmem) + 256 * X;   // uniform for the compiler as well
-    const uint64_t q_desc = sw128_desc(smem_u32(q_s + X * S_::kQTile), 16, 1024);
+    const uint32_t tm = __reduce_max_sync(FULL, tmem);   // uniform for the compiler as well
+    const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
     const uint64_t k_desc = sw128_desc(smem_u32(k16), 16, 1024);
     const uint64_t v_desc = sw128_desc(smem_u32(v16), kSlab, 1024);
-    RingPos<kBufK> kp;   // of the next Q K^T
-    RingPos<kBufV> vp;   // of the next P V
-    RingPos<2> sq, sp;   // S / P buffers of the next Q K^T and the next P V
-    int units = 0;       // of this tile so far
-    Work w;
-    for (int k = 0; next_work(k, w); ++k) {
-      const int nt = X ? w.nt[1] : w.nt[0], steps = w.steps;
-      // steps [inner0, inner1) have no V row that nobody sees
-      const int inner0 = (w.keys.ns + (w.keys.wb * kChunkKeys < w.keys.w0) + kStepChunks - 1) / kStepChunks;
-      const int inner1 = (w.keys.ns + max((w.keys.last + 1) / kChunkKeys - w.keys.wb, 0)) / kStepChunks;
-      release_work(k);
-      auto qk = [&](bool last) {
-        const int i = 2 * X + sq.slot;
-        wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par);
-        // the buffer's step before: its P has been read by P V
-        if (sq.used) wait(&o_done[i], sq.par ^ 1);
-        tc_fence_after();
-        const uint64_t kd = k_desc + static_cast<uint32_t>(kp.slot * (S_::kStrideK >> 4));
-        const uint32_t d_tmem = tm + 64 * sq.slot;
+    // S of a step of tile X from K buffer `slot`, into buffer `to` of the tile
+    auto qk = [&](int X, int slot, int to) {
+      const uint64_t kd = k_desc + static_cast<uint32_t>(slot * (S_::kStrideK >> 4));
+      const uint32_t d_tmem = tm + 256 * X + 64 * to;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(leader, d_tmem, q_desc + (((ks >> 2) * kQSlab + 32 * (ks & 3)) >> 4),
-                 kd + (((ks >> 2) * kSlab + 32 * (ks & 3)) >> 4), kIdQK, ks > 0 ? 1u : 0u);
-        commit(leader, smem_u32(&s_full[i]));
-        if (kFp8) commit(leader, smem_u32(&k_free[kp.slot]));
-        if (last) commit(leader, smem_u32(&q_free[X]));
-        kp.next();
-        sq.next();
-      };
-      auto pv = [&](int t) {
-        const int i = 2 * X + sp.slot;
-        // V rows that nobody sees (16-bit caches; the helpers leave zeros), while
-        // P is made: both tiles write the same zeros, each before its own P V
-        if constexpr (!kFp8) {
-          if (t < inner0 || t >= inner1) {
+      for (int ks = 0; ks < D / 16; ++ks)
+        mma_ss(leader, d_tmem, q_desc + ((X * S_::kQTile + (ks >> 2) * kQSlab + 32 * (ks & 3)) >> 4),
+               kd + (((ks >> 2) * kSlab + 32 * (ks & 3)) >> 4), kIdQK, ks > 0 ? 1u : 0u);
+      commit(leader, smem_u32(&s_full[2 * X + to]));
+    };
+    // O += P V of a step of tile X, P in buffer `from`, V in buffer `slot`
+    auto pv = [&](int X, int slot, int from, bool first) {
+      const uint64_t vd = v_desc + static_cast<uint32_t>(slot * (S_::kStrideV >> 4));
+      const uint32_t o_tmem = tm + 256 * X + 128, p_tmem = tm + 256 * X + 64 * from;
+#pragma unroll
+      for (int kk = 0; kk < kKeys / 16; ++kk)
+        mma_ts(leader, o_tmem, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
+      commit(leader, smem_u32(&o_done[2 * X + from]));
+    };
+    // The work is split by tile for E4M3 caches and by product for 16-bit ones:
+    //   one prompt of 8,192, window 2,048, bf16: 198 us by tile, 190 by product
+    //   16 chunks of 512, window 1,024, bf16:     91 us,           86
+    //   16 block-scaled chunks of 512:           270 us,          340
+    // By product no warp waits for a P V before it comes to the next Q K^T, but
+    // the tiles keep step, and both wait when a widened buffer comes late.
+    Work w;
+    if constexpr (kFp8) {
+      const int X = warp - kMmaWarp;
+      RingPos<kBufK> kp;   // of the next Q K^T
+      RingPos<kBufV> vp;   // of the next P V
+      RingPos<2> sq, sp;   // S / P buffers of the next Q K^T and the next P V
+      int units = 0;       // of this tile so far
+      for (int k = 0; next_work(k, w); ++k) {
+        const int nt = X ? w.nt[1] : w.nt[0], steps = w.steps;
+        release_work(k);
+        auto next_qk = [&](bool last) {
+          wait(&k_full[kp.slot], kp.par);
+          // the buffer's step before: its P has been read by P V
+          if (sq.used) wait(&o_done[2 * X + sq.slot], sq.par ^ 1);
+          tc_fence_after();
+          qk(X, kp.slot, sq.slot);
+          commit(leader, smem_u32(&k_free[kp.slot]));
+          if (last) commit(leader, smem_u32(&q_free[X]));
+          kp.next();
+          sq.next();
+        };
+        if (nt > 0) {
+          wait(&q_full[X], units & 1);
+          next_qk(nt == 1);
+          if (nt > 1) next_qk(nt == 2);
+          for (int t = 0; t < nt; ++t) {
+            // O of the unit before has been read
+            if (t == 0 && units > 0) wait(&o_free[X], (units - 1) & 1);
+            wait(&p_full[2 * X + sp.slot], sp.par);
+            tc_fence_after();
+            pv(X, vp.slot, sp.slot, t == 0);
+            commit(leader, smem_u32(&v_free[vp.slot]));
+            vp.next();
+            sp.next();
+            if (t + 2 < nt) next_qk(t + 3 == nt);
+          }
+          ++units;
+        }
+        // the stream's steps that only the other tile reads
+        for (int t = nt; t < steps; ++t) {
+          wait(&k_full[kp.slot], kp.par);
+          wait(&v_full[vp.slot], vp.par);
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&k_free[kp.slot]));
+            mbar_arrive(smem_u32(&v_free[vp.slot]));
+          }
+          kp.next();
+          vp.next();
+        }
+        if (__any_sync(FULL, late)) {
+          give_up();
+          break;
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      RingPos<kRing> at;       // stage of the stream
+      RingPos<2> buf[2];       // each tile's next S / P buffer
+      int units[2] = {0, 0};   // of each tile so far
+      for (int k = 0; next_work(k, w); ++k) {
+        const int nt[2] = {w.nt[0], w.nt[1]}, steps = w.steps;
+        release_work(k);
+        for (int t = 0; t < steps; ++t) {
+          wait(&full[at.slot], at.par);
+#pragma unroll
+          for (int X = 0; X < 2; ++X) {
+            if (t >= nt[X]) continue;
+            if (t == 0) wait(&q_full[X], units[X] & 1);
+            // the buffer's step before: its P has been read by P V
+            if (buf[X].used) wait(&o_done[2 * X + buf[X].slot], buf[X].par ^ 1);
+            tc_fence_after();
+            qk(X, at.slot, buf[X].slot);
+            if (t + 1 == nt[X]) commit(leader, smem_u32(&q_free[X]));
+            buf[X].next();
+          }
+          at.next();
+        }
+        units[0] += nt[0] > 0;
+        units[1] += nt[1] > 0;
+        if (__any_sync(FULL, late)) {
+          give_up();
+          break;
+        }
+      }
+    } else {
+      RingPos<kRing> at;
+      RingPos<2> buf[2];
+      int units[2] = {0, 0};
+      for (int k = 0; next_work(k, w); ++k) {
+        const int nt[2] = {w.nt[0], w.nt[1]}, steps = w.steps;
+        const Keys keys = w.keys;
+        // steps [inner0, inner1) have no V row that nobody sees
+        const int inner0 = (keys.ns + (keys.wb * kChunkKeys < keys.w0) + kStepChunks - 1) / kStepChunks;
+        const int inner1 = (keys.ns + max((keys.last + 1) / kChunkKeys - keys.wb, 0)) / kStepChunks;
+        release_work(k);
+        for (int t = 0; t < steps; ++t) {
+          if (t < inner0 || t >= inner1) {   // such rows become zeros while P is made
             constexpr int kPieces = 8 * S_::kSlabs;   // 16-byte pieces of a row, a lane each
-            uint8_t* vt = ring + vp.slot * S_::kStage + S_::kTile + (lane % kPieces >> 3) * kSlab + (lane & 7) * 16;
+            uint8_t* vt = ring + at.slot * S_::kStage + S_::kTile + (lane % kPieces >> 3) * kSlab + (lane & 7) * 16;
+            wait(&full[at.slot], at.par);
             __syncwarp();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int c = w.keys.chunk(kStepChunks * t + 2 * h + (lane >> 4));
-              const uint32_t none = __ballot_sync(FULL, !w.keys.any_sees(c * kChunkKeys + (lane & 15)));
+              const int c = keys.chunk(kStepChunks * t + 2 * h + (lane >> 4));
+              const uint32_t none = __ballot_sync(FULL, !keys.any_sees(c * kChunkKeys + (lane & 15)));
               if (none != 0)
                 for (int r = lane / kPieces; r < 32; r += 32 / kPieces)
                   if (none >> r & 1u)
@@ -618,45 +703,26 @@ __global__ void __launch_bounds__(kThreadsW, 1)
             fence_proxy_async();   // before the tensor core reads V
             __syncwarp();
           }
-        }
-        // O of the unit before has been read
-        if (t == 0 && units > 0) wait(&o_free[X], (units - 1) & 1);
-        wait(&p_full[i], sp.par);
-        tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint32_t>(vp.slot * (S_::kStrideV >> 4));
-        const uint32_t p_tmem = tm + 64 * sp.slot;
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(leader, tm + 128, p_tmem + 8 * kk, vd + ((2048 * kk) >> 4), kIdPV, (t > 0 || kk > 0) ? 1u : 0u);
-        commit(leader, smem_u32(&o_done[i]));
-        commit(leader, smem_u32(kFp8 ? &v_free[vp.slot] : &empty[vp.slot]));
-        vp.next();
-        sp.next();
-      };
-      if (nt > 0) {
-        wait(&q_full[X], units & 1);
-        qk(nt == 1);
-        if (nt > 1) qk(nt == 2);
-        for (int t = 0; t < nt; ++t) {
-          pv(t);
-          if (t + 2 < nt) qk(t + 3 == nt);
+          for (int X = 0; X < 2; ++X) {
+            if (t >= nt[X]) continue;
+            // O of the unit before has been read
+            if (t == 0 && units[X] > 0) wait(&o_free[X], (units[X] - 1) & 1);
+            wait(&p_full[2 * X + buf[X].slot], buf[X].par);
+            tc_fence_after();
+            pv(X, at.slot, buf[X].slot, t == 0);
+            buf[X].next();
+          }
+          // (the stage's K has been read as well: P follows from S)
+          commit(leader, smem_u32(&empty[at.slot]));
+          at.next();
         }
-        ++units;
-      }
-      // the stream's steps that only the other tile reads
-      for (int t = nt; t < steps; ++t) {
-        wait(kFp8 ? &k_full[kp.slot] : &full[kp.slot], kp.par);
-        if (kFp8) wait(&v_full[vp.slot], vp.par);
-        if (lane == 0) {
-          if (kFp8) mbar_arrive(smem_u32(&k_free[kp.slot]));
-          mbar_arrive(smem_u32(kFp8 ? &v_free[vp.slot] : &empty[vp.slot]));
+        units[0] += nt[0] > 0;
+        units[1] += nt[1] > 0;
+        if (__any_sync(FULL, late)) {
+          give_up();
+          break;
         }
-        kp.next();
-        vp.next();
-      }
-      if (__any_sync(FULL, late)) {
-        give_up();
-        break;
       }
     }
     commit(leader, smem_u32(&fin));

@@ -27,6 +27,13 @@
 // block-scaled cache is one warp's (two for blocks of 32; D / 16 lanes where
 // there is one new token): the maximum is a reduction over its lanes, and
 // nobody else writes that block's bytes or its scale.
+//
+// Measured (GB300; a plain copy reaches 6,779 GB/s):
+//   64 new tokens, 28 query / 4 KV heads, bf16:                 3.7 us (latency: the table entry, then the row)
+//   6,400 tokens of chunks, 28 / 4 heads, bf16:                24.4 us, 5,590 GB/s
+//   512 new tokens, 64 / 8 heads, into a block-scaled cache:    5.5 us, 3,670 GB/s
+//   40,000 tokens of prompts, 64 / 8 heads, block-scaled:       260 us, 5,910 GB/s
+// DRAM counters of the last: 0.82 GB read and 0.68 GB written, what it has to.
 #include <algorithm>
 #include <type_traits>
 

@@ -29,6 +29,16 @@
 // Sums, maxima and O are fp32; q and P are rounded to the MMA's 16-bit type
 // (the cache's, f16 for E4M3), off by a relative 2^-8 (bf16) or 2^-11 (f16) at
 // most.
+//
+// Measured (GB300; a plain copy reaches 6,779 GB/s), visible K/V bytes:
+//   8 contexts of 16,384 to 32,768, 32 / 32 heads, window 4,096, f16:  81 us, 6,670 GB/s
+//   512 block-scaled contexts of 64 to 8,192, 64 / 8 heads:           293 us, 5,850 GB/s
+//   64 contexts of 256 to 4,096, 28 / 4 heads, window 1,024, bf16:     26 us, 4,810 GB/s
+//   4 block-scaled contexts of up to 128, 32 / 8 heads:               4.3 us
+// DRAM counters agree with the visible bytes within 3%.  Short calls are
+// latency: a chunk is about 0.85 us of one warp (copy, two MMA chains, softmax
+// between), whatever the depth of its ring, and a launch with a unit's first
+// lookups about 3 us.
 #pragma once
 
 #include <atomic>

@@ -5,7 +5,7 @@
 // sees p' <= p with p' > p - window or p' < sinks (window 0: every p' <= p).
 //   out = softmax(q . K^T * scale) V  over what it sees.
 //
-// A CTA takes 256 query rows of one KV head as two tiles of 128 (M of an
+// A unit of work is 256 query rows of one KV head as two tiles of 128 (M of an
 // MMA).  Row r of a chunk is head r % G of position r / G: the G query heads
 // that share a KV head share its K/V tiles, and 256 rows span 256 / G
 // positions only, so that with a window little more than its own keys is
@@ -13,8 +13,11 @@
 // four chunks of 16 each: the sinks' chunks, then those from the first row's
 // window on; blocks between are not looked up.
 //
-// Warps 0-3 and 4-7 do the softmax of tile A and B (a thread a row, TMEM lane
-// = row), warp 8 drives TMA, warp 9 issues the MMAs:
+// One CTA of 16 warps lives on each SM and claims units as it goes (cluster
+// launch control).  Warps 0-3 and 4-7 do the softmax of tile A and B (a thread
+// a row, TMEM lane = row), warp 8 drives TMA, warps 9 and 10 issue the MMAs,
+// warp 11 claims and describes units, warps 12-15 load queries, widen E4M3 and
+// write the output of a unit while the next one runs:
 //   S_t = Q K_t^T  (128 x 64, into one of two TMEM buffers per tile)
 //   P_t = 2^(S_t scale - m)  (16 bit, over the S buffer it came from)
 //   O  += P_t V_t  (128 x D, A operand from TMEM)
@@ -23,6 +26,18 @@
 // its running maximum has grown by 2^8, and then its O is rescaled.  The pool
 // rows (and scales) of 32 chunks are fetched a lane each, a batch ahead, and
 // the boxes of a step go out a lane each.
+//
+// Measured (GB300, 152 SMs), of 1870 TFLOP/s that a library product reaches:
+//   one prompt of 8,192, 32 query / 8 KV heads, window 2,048, bf16:  190 us, 1265 TFLOP/s
+//   16 chunks of 512, 28 / 4 heads, window 1,024, bf16:               86 us, 1020 TFLOP/s
+//   16 block-scaled E4M3 chunks of 512 over 1,024 to 4,096 tokens:   239 us,  920 TFLOP/s
+// What bounds it: a step of both tiles takes 1,300 to 1,450 cycles.  With N =
+// 64 its Q K^T reads 6 KB of shared memory per MMA of 32 tensor cycles (1,280
+// cycles a step at 128 bytes a cycle, with P V); the 16 TMA boxes of a step
+// cost their warp about 80 cycles each; and the two issuing warps wait on
+// barriers between.  Half the MMA work alone takes 4% off, a quarter of the
+// boxes alone 3%, both 16%.  Keys in steps of 128 do not fit TMEM beside O
+// with two buffers.
 //
 // E4M3 caches are widened to f16 in shared memory by four warps.  With block
 // scales a step has one power of two R per K and V, the exponent of the

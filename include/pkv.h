@@ -566,7 +566,8 @@ typedef struct {
  * its tokens unwritten and sets PKV_DEVICE_BAD_TABLE.  Without query_start a
  * sequence of context 0 writes nothing and gets a zero q_out row.  Rows outside
  * [query_start[0], query_start[num_seqs]) and outside [0, total_tokens) are
- * left alone.  Launched with programmatic stream serialization, like the
+ * left alone; a query_start that decreases or leaves [0, total_tokens] sets
+ * PKV_DEVICE_BAD_LENGTH.  Launched with programmatic stream serialization, like the
  * tensor-core decode kernels; asynchronous on `stream`. */
 PKV_API pkv_status pkv_append(void* k_cache, void* v_cache, float* block_scales, const void* k,
                               int64_t k_stride, const void* v, int64_t v_stride, void* q_out,

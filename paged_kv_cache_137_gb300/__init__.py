@@ -870,7 +870,8 @@ def pkv_append(k_cache, v_cache, k, v, block_tables, context_lens, desc: pkv_kv_
     """Write each sequence's new tokens at its last positions, K and q rotated
     by them (pkv_append).  k, v [n, N_kv, D] and q [n, Hq, D] may be views of a
     packed projection; query_start int32[B + 1] gives each sequence's rows
-    (None: one token each).  Returns q_out."""
+    (None: one token each).  Without max_query_len the longest chunk is read
+    back from the device (so give it when capturing).  Returns q_out."""
     _check(lib().pkv_append(*_append_args(k_cache, v_cache, k, v, block_tables, context_lens, desc, query_start,
                                           max_query_len, rope, q, q_out, block_scales, k_inv_scale,
                                           v_inv_scale), _stream(stream)))

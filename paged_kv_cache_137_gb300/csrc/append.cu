@@ -75,7 +75,7 @@ struct AppendArgs {
 // first ..; n = 0 where there is nothing to write.
 struct Chunk {
   int32_t row0, n, first;
-  bool bad;   // invalid lengths: nothing is written, its q_out rows become NaN
+  bool bad;   // invalid lengths: nothing is written, its q_out rows (n of them) become NaN
 };
 __device__ __forceinline__ Chunk chunk_of(const AppendArgs& a, int s) {
   Chunk c{s, 1, 0, false};
@@ -84,7 +84,7 @@ __device__ __forceinline__ Chunk chunk_of(const AppendArgs& a, int s) {
     c.row0 = a.query_start[s];
     const int end = a.query_start[s + 1];
     // rows outside the inputs: nothing this call may touch
-    if (c.row0 < 0 || end <= c.row0 || end > a.total) return {0, 0, 0, false};
+    if (c.row0 < 0 || end < c.row0 || end > a.total) return {0, 0, 0, true};
     c.n = end - c.row0;
   } else if (ctx == 0) {
     c.first = -1;   // no token: the q_out row becomes zero
@@ -231,7 +231,10 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int cta) {
     in_chunk = t;
   }
   const Chunk c = chunk_of(a, seq);
-  if (in_chunk >= c.n) return;
+  if (in_chunk >= c.n) {
+    if (c.bad && c.n == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
+    return;
+  }
   const size_t tok = static_cast<size_t>(c.row0) + in_chunk;
   if (c.bad || c.first < 0) {
     if (c.bad && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
@@ -424,11 +427,11 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int seq, int j
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % kUnits, sub = lane / kUnits;
   const int T = a.block_size, warps = T / 16;
   const Chunk c = chunk_of(a, seq);
-  if (c.n == 0) return;
   if (c.bad) {
     if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEVICE_BAD_LENGTH);
     return;
   }
+  if (c.n == 0) return;
   const int lb = c.first / T + j;
   const int end = c.first + c.n;
   if (static_cast<int64_t>(lb) * T >= end) return;

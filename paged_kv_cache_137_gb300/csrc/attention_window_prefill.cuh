@@ -398,8 +398,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         my_q0 = a.query_start[lane];
         my_n = a.query_start[lane + 1] - my_q0;
         my_ctx = a.ctx_lens[lane];
-        if (my_q0 >= 0 && my_n > 0 && my_n <= a.total_q - my_q0)   // else no rows this call may write
+        if (my_q0 >= 0 && my_n >= 0 && my_n <= a.total_q - my_q0)
           my_units = static_cast<int>((static_cast<int64_t>(my_n) * G + kUnitRows - 1) / kUnitRows);
+        else if (a.status != nullptr)   // rows outside the inputs: none that this call may write
+          atomicOr(a.status, kBadLength);
       }
       for (int o = 0; o < a.num_seqs; ++o) {
         const int ctx = __shfl_sync(FULL, my_ctx, o), units = __shfl_sync(FULL, my_units, o);
@@ -461,7 +463,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
           n = a.query_start[lo + 1] - q0;
           ctx = a.ctx_lens[lo];
           at = slot - slot0(lo);
-          if (at < 0 || q0 < 0 || n <= 0 || n > a.total_q - q0) continue;   // no rows this call may write
+          if (q0 < 0 || n < 0 || n > a.total_q - q0) {   // rows outside the inputs: none that this call may write
+            if (lane == 0 && a.status != nullptr) atomicOr(a.status, kBadLength);
+            continue;
+          }
+          if (at < 0) continue;
           pairs = static_cast<int>((static_cast<int64_t>(n) * G + kUnitRows - 1) / kUnitRows);
           if (at >= pairs) continue;
         }

@@ -321,6 +321,22 @@ def test_prepared_captured_and_on_another_stream(kv):
     assert sa is None or torch.equal(sa, sb)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("start", [[0, 5, 3, 9], [0, 5, 9, 60], [-2, 0, 4, 9]])
+def test_a_query_start_out_of_order_sets_the_status(kv, start):
+    """Chunks outside the inputs write nothing and say so; nothing else is hurt."""
+    b = Batch([20, 30, 19], [5, 4, 0], kv=kv, seed=4)
+    b.start = torch.tensor(start, dtype=torch.int32, device="cuda")
+    scales = torch.ones((b.nb, b.hkv, 2), device="cuda") if kv == "e4m3" else None
+    b.call(block_scales=scales, max_query_len=9)
+    assert pkv.pkv_device_status(clear=True) == pkv.PKV_DEVICE_BAD_LENGTH
+    whole = [s for s in range(3) if 0 <= start[s] <= start[s + 1] <= b.total]
+    for cache, before in ((b.k_cache, b.before[0]), (b.v_cache, b.before[1])):
+        same = torch.as_tensor(before).view(torch.uint8).flatten(1).eq(cache.cpu().view(torch.uint8).flatten(1))
+        changed = {int(i) for i in torch.nonzero(~same.all(dim=1)).flatten()}
+        assert changed <= {int(x) for s in whole for x in b.tables[s] if x >= 0}
+
+
 def test_a_rope_filled_by_hand():
     a, b = (Batch(CTX, [1] * len(CTX), seed=9) for _ in range(2))
     b.rope = pkv.pkv_rope(b.table.data_ptr(), b.table.shape[0], b.table.shape[1], 0)

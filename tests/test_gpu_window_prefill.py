@@ -211,3 +211,24 @@ def test_offsets_past_32_bits(scales):
             setattr(x, name, big)
     x.tables_d = torch.where(x.tables_d >= 0, x.tables_d + (nb - x.nb), x.tables_d).int()
     assert torch.equal(attend(x), want)
+
+
+@pytest.mark.parametrize("seqs", [3, 40])
+def test_a_query_start_out_of_order_sets_the_status(seqs):
+    """Few and many sequences: a chunk outside the inputs is not written and says so."""
+    x = Inputs([60] * seqs, [10] * seqs, hq=4, hkv=2, kv="bf16", window=50, sinks=4, seed=2)
+    x.start[-1] = x.total + 30
+    out = torch.full_like(x.q_d, 7.0)
+    attend(x, out=out)
+    assert pkv.pkv_device_status(clear=True) == pkv.PKV_DEVICE_BAD_LENGTH
+    assert (out[-10:] == 7).all() and not (out[:-10] == 7).all(dim=(1, 2)).any()
+
+
+@pytest.mark.parametrize("seqs", [31, 32, 33, 70])
+def test_many_sequences(seqs):
+    """The scheduler ranks up to 32 sequences and searches among more."""
+    r = np.random.RandomState(seqs)
+    ctx = r.randint(1, 200, size=seqs)
+    x = Inputs(ctx, [int(r.randint(0, c + 1)) for c in ctx], hq=6, hkv=2, kv="bf16", window=64, sinks=3, seed=seqs)
+    x.check(attend(x))
+    assert pkv.pkv_device_status() == 0

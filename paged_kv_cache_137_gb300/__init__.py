@@ -233,11 +233,14 @@ def _dev(t: torch.Tensor, name: str, dtype=None):
     return t.data_ptr()
 
 
+_CODE_OF_TORCH = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    m = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
-    if t.dtype not in m:
+    code = _CODE_OF_TORCH.get(t.dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 # ------------------------------------------------------------------ sizing

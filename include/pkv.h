@@ -606,8 +606,8 @@ PKV_API size_t pkv_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
  * 1): arguments, workspace (of pkv_window_workspace_bytes), splits, launch and
  * errors as there; the query of sequence s is at position context_lens[s] - 1.
  * partition_tokens counts visible tokens, a multiple of 64 (0: automatic).
- * The tensor-core kernel takes 16-bit caches and E4M3 caches with head_dim
- * 128, the CUDA-core kernel the others; pkv_set_attention_kernel applies. */
+ * The tensor-core kernel takes 16-bit and E4M3 caches, the CUDA-core kernel
+ * fp32 ones; pkv_set_attention_kernel applies. */
 PKV_API pkv_status pkv_attention_decode_window(
     void* out, const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens, int32_t num_seqs,

@@ -117,7 +117,6 @@ pkv_status plan_window(const pkv_kv_desc* d, int32_t num_seqs, int32_t num_q_hea
 // Whether the tensor-core kernel covers these sizes.
 bool window_tc_covers(const pkv_kv_desc* d) {
   if (d->kv_dtype == PKV_F32) return false;
-  if (d->kv_dtype == PKV_E4M3 && d->head_dim != 128) return false;
   return static_cast<int64_t>(d->num_blocks) * d->num_kv_heads * d->block_size <= INT32_MAX;
 }
 
@@ -213,10 +212,15 @@ pkv_status decode_window_impl(void* out, const void* q, int32_t q_dtype, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int D = desc->head_dim;
   if (tc) {
-    // boxes of 16 rows whatever the block size: the pool as blocks of 16
+    // boxes of 16 rows whatever the block size: the pool as blocks of 16 (rows
+    // of 64 bytes in pairs: eight of 128)
     pkv_kv_desc by16 = *desc;
     by16.num_blocks = desc->num_blocks * (desc->block_size / 16);
     by16.block_size = 16;
+    if (D * pkv_dtype_bytes(kv) == 64) {
+      by16.head_dim = 2 * D;
+      by16.block_size = 8;
+    }
     CUtensorMap kmap, vmap;
     st = pool_map(&kmap, k_cache, &by16);
     if (st == PKV_OK) st = pool_map(&vmap, v_cache, &by16);

@@ -52,6 +52,29 @@ namespace tc {
 
 constexpr int kChunk = 16;   // tokens of a chunk: the MMA's rows
 
+// A chunk of K or V in shared memory: its rows in lines of 128 bytes, swizzled
+// by TMA.  A line is half a 256-byte row, a row, or two rows of 64 bytes (the
+// pool seen as rows of 128): ldmatrix meets eight different bank groups each way.
+template <typename KV, int D>
+struct ChunkGeom {
+  static constexpr int kRowBytes = D * KV::bytes;
+  static constexpr int kPieces = kRowBytes / 16;   // 16-byte pieces of a row
+  static constexpr int kLineRows = kRowBytes < 128 ? 128 / kRowBytes : 1;
+  static constexpr int kTileBytes = kChunk * kRowBytes;
+  static constexpr int kStageBytes = 2 * kTileBytes;   // K and V
+  static_assert(kTileBytes % 1024 == 0, "the swizzle repeats every 1024 bytes");
+  // piece c of row r
+  __device__ static __forceinline__ uint32_t at(int r, int c) {
+    if constexpr (kLineRows == 1) return swz<kRowBytes / 128>(r, c);
+    else return swz<1>(r / kLineRows, r % kLineRows * kPieces + c);
+  }
+  // the box of the chunk that starts at pool row `row`
+  __device__ static __forceinline__ void fetch(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+    if constexpr (kRowBytes <= 128) tma_load_2d(dst, map, 0, row / kLineRows, bar);
+    else tma_load_3d(dst, map, 0, 0, row, bar);
+  }
+};
+
 // The visible positions of a query at position ctx - 1, as chunks.
 struct Span {
   int ctx, w0, s0;   // positions [0, s0) and [w0, ctx)
@@ -111,19 +134,19 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH>& st,
                                            const uint32_t (&qb)[NH][D / 16][2], const uint8_t* kt,
                                            uint8_t* vt, const Span& span, int pos, float qk, float vs,
                                            int lane) {
-  using G_ = Geom<KV, D>;
+  using G_ = ChunkGeom<KV, D>;
   constexpr bool kFp8 = std::is_same<KV, E4M3>::value;
   constexpr bool kBf = std::is_same<KV, BF16>::value;
-  constexpr int KS = D / 16, S = G_::kSlabs;
+  constexpr int KS = D / 16, P = G_::kPieces;
   constexpr unsigned FULL = 0xffffffffu;
   const int g = lane >> 2;
   bool zeroed = false;
   const bool whole = span.sees_all(pos);
   if (!whole) {   // a weight of 0 times what an unseen row holds must be 0
-    for (int i = lane; i < kChunk * S * 8; i += 32) {
-      const int r = i / (S * 8);
+    for (int i = lane; i < kChunk * P; i += 32) {
+      const int r = i / P;
       if (!span.sees(pos + r))
-        *reinterpret_cast<uint4*>(vt + swz<S>(r, i % (S * 8))) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(vt + G_::at(r, i % P)) = make_uint4(0, 0, 0, 0);
     }
     __syncwarp();
     zeroed = true;
@@ -143,7 +166,7 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH>& st,
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t a0, a1, a2, a3;
-      ldsm_x4(kbase + swz<S>(rk, 2 * ks + (mi >> 1)), a0, a1, a2, a3);
+      ldsm_x4(kbase + G_::at(rk, 2 * ks + (mi >> 1)), a0, a1, a2, a3);
 #pragma unroll
       for (int h = 0; h < NH; ++h)
         mma16816<kBf>(ks & 1 ? sd[h] : sc[h], a0, a1, a2, a3, qb[h][ks][0], qb[h][ks][1]);
@@ -152,7 +175,7 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH>& st,
 #pragma unroll
     for (int ks = 0; ks < KS; ks += 2) {   // one load serves two k-steps
       uint32_t w[4];
-      ldsm_x4(kbase + swz<S>(rk, ks + (mi >> 1)), w[0], w[1], w[2], w[3]);
+      ldsm_x4(kbase + G_::at(rk, ks + (mi >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t a0 = e4m3x2_f16x2(w[2 * k] & 0xffffu), a1 = e4m3x2_f16x2(w[2 * k + 1] & 0xffffu);
@@ -217,7 +240,7 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH>& st,
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
       uint32_t a0, a1, a2, a3;
-      ldsm_x4_t(vbase + swz<S>(rv, 2 * mt + (mi & 1)), a0, a1, a2, a3);
+      ldsm_x4_t(vbase + G_::at(rv, 2 * mt + (mi & 1)), a0, a1, a2, a3);
 #pragma unroll
       for (int h = 0; h < NH; ++h) mma16816<kBf>(st.o[h][mt], a0, a1, a2, a3, pb[h][0], pb[h][1]);
     }
@@ -226,7 +249,7 @@ __device__ __forceinline__ bool chunk_step(WindowState<D, NH>& st,
 #pragma unroll
     for (int mt = 0; mt < D / 16; mt += 2) {
       uint32_t w[4];   // (tokens 0-7, mt), (8-15, mt), (0-7, mt + 1), (8-15, mt + 1)
-      ldsm_x4_t(vbase + swz<S>(rk, mt + (mi >> 1)), w[0], w[1], w[2], w[3]);
+      ldsm_x4_t(vbase + G_::at(rk, mt + (mi >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t x0 = prmt(w[2 * k], 0x3120), x1 = prmt(w[2 * k + 1], 0x3120);
@@ -318,14 +341,14 @@ __device__ __forceinline__ void finish_unit(const WindowArgs& a, const float* mS
 template <typename KV, int D, int NH>
 constexpr int window_warps(int c) {
   // (two column sets of heads leave registers for 12 warps as well)
-  constexpr bool wide = NH > 1 || Geom<KV, D, 1>::kStageBytes >= 8192;
+  constexpr bool wide = NH > 1 || ChunkGeom<KV, D>::kStageBytes >= 8192;
   return c <= 1 ? (wide ? 12 : 16) : c == 2 ? (wide ? 6 : 8) : kWarps;
 }
 template <typename KV, int D>
-constexpr int window_stages() { return Geom<KV, D, 1>::kStageBytes >= 8192 ? 2 : 3; }
+constexpr int window_stages() { return ChunkGeom<KV, D>::kStageBytes >= 8192 ? 2 : 3; }
 template <typename KV, int D, int NH, int W>
 constexpr int window_ctas() {
-  constexpr int warps = NH == 1 && Geom<KV, D, 1>::kStageBytes < 8192 ? 16 : 12;
+  constexpr int warps = NH == 1 && ChunkGeom<KV, D>::kStageBytes < 8192 ? 16 : 12;
   return warps / W < 1 ? 1 : warps / W;
 }
 
@@ -333,7 +356,7 @@ template <typename KV, typename Q, int D, int NH, bool BS, int W>
 __global__ void __launch_bounds__(32 * W, window_ctas<KV, D, NH, W>())
     decode_window_kernel(const WindowArgs a, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap) {
-  using G_ = Geom<KV, D, 1>;   // one warp's stage: 16 tokens of K, then of V
+  using G_ = ChunkGeom<KV, D>;   // one warp's stage: 16 tokens of K, then of V
   constexpr int NS = window_stages<KV, D>();
   constexpr int KS = D / 16;
   constexpr unsigned FULL = 0xffffffffu;
@@ -407,8 +430,7 @@ __global__ void __launch_bounds__(32 * W, window_ctas<KV, D, NH, W>())
     if (lane == 0) mbar_arrive_expect_tx(b, row >= 0 ? G_::kStageBytes : 0);
     __syncwarp();
     if (lane < 2 && row >= 0)
-      tma_box<KV, D>(smem_u32(ring + slot * G_::kStageBytes + lane * G_::kTileBytes),
-                     lane ? &vmap : &kmap, row, b);
+      G_::fetch(smem_u32(ring + slot * G_::kStageBytes + lane * G_::kTileBytes), lane ? &vmap : &kmap, row, b);
   };
   for (int i = 0; i < NS && i < n; ++i) issue(i, 0, i);
   fetch(1, row_nxt, sc_nxt);
@@ -470,7 +492,7 @@ __global__ void __launch_bounds__(32 * W, window_ctas<KV, D, NH, W>())
 template <typename KV, typename Q, int D, int NH, bool BS, int W>
 pkv_status launch_window_form(const WindowArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               cudaStream_t st) {
-  constexpr int smem = W * window_stages<KV, D>() * Geom<KV, D, 1>::kStageBytes + 1024;
+  constexpr int smem = W * window_stages<KV, D>() * ChunkGeom<KV, D>::kStageBytes + 1024;
   auto kernel = decode_window_kernel<KV, Q, D, NH, BS, W>;
   static std::atomic<uint64_t> configured{0};   // the shared-memory opt-in is per device
   int dev = 0;
@@ -519,8 +541,7 @@ template <typename KV, typename Q>
 pkv_status launch_window_tc(const WindowArgs& a, int head_dim, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, cudaStream_t st) {
   if (head_dim == 128) return tc::launch_window_d<KV, Q, 128>(a, kmap, vmap, st);
-  if constexpr (!std::is_same<KV, E4M3>::value)
-    if (head_dim == 64) return tc::launch_window_d<KV, Q, 64>(a, kmap, vmap, st);
+  if (head_dim == 64) return tc::launch_window_d<KV, Q, 64>(a, kmap, vmap, st);
   return fail(PKV_ERR_UNSUPPORTED, "windowed decode: head_dim not compiled for the tensor-core kernel");
 }
 

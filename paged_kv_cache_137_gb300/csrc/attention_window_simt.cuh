@@ -1,6 +1,5 @@
 // CUDA-core form of windowed and block-scaled decode attention: fp32 caches,
-// E4M3 caches with head_dim 64, and any other shape when the CUDA-core kernels
-// are asked for.  The same chunks, splits and merge as attention_window.cuh; a
+// and any other when the CUDA-core kernels are asked for.  The same chunks, splits and merge as attention_window.cuh; a
 // warp takes every fourth chunk of its split, two lanes share a token in the
 // q.k phase (head_dim / 2 elements each) and the lanes split head_dim for
 // p.V.  All G heads (padded to GM) go together, so a K/V element is read once

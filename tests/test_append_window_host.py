@@ -175,7 +175,6 @@ def test_decode_refuses():
     pkv.pkv_set_attention_kernel("tc")
     try:
         refused(attend("decode", False, desc=desc_of("f32"), q_dtype=F32), UNSUPPORTED, "tensor-core")
-        refused(attend("decode", True, desc=desc_of("e4m3", d=64)), UNSUPPORTED, "tensor-core")
     finally:
         pkv.pkv_set_attention_kernel("auto")
 

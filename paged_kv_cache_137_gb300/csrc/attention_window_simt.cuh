@@ -13,7 +13,9 @@ namespace pkv {
 template <typename KV, typename Q, int D, int GM>
 __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const WindowArgs a) {
   using namespace tc;
-  constexpr int DQ = D / 2, DV = D / 32, KCH = 8;
+  constexpr int DQ = D / 2, DV = D / 32;
+  constexpr int KB = 32;        // K elements a lane has in flight
+  constexpr int VB = 32 / DV;   // V rows (of DV elements a lane) in flight
   constexpr unsigned FULL = 0xffffffffu;
   using raw = typename KV::raw;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -52,10 +54,13 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
     for (int e = 0; e < DV; ++e) acc[j][e] = 0.f;
   }
   const int tok = lane % kChunk, part = lane / kChunk;
+  const int32_t* trow = a.tables + static_cast<size_t>(seq) * a.max_blocks;
   bool bad = false;
+  int next = c0 + warp < c1 ? trow[span.chunk(c0 + warp) * kChunk / T] : 0;
   for (int c = c0 + warp; c < c1; c += kWarps) {
     const int pos = span.chunk(c) * kChunk;
-    const int blk = a.tables[static_cast<size_t>(seq) * a.max_blocks + pos / T];
+    const int blk = next;
+    if (c + kWarps < c1) next = trow[span.chunk(c + kWarps) * kChunk / T];
     if (blk < 0 || blk >= a.num_blocks) {   // the same for the whole warp
       bad = true;
       break;
@@ -70,15 +75,28 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
     float s[GM];
 #pragma unroll
     for (int j = 0; j < GM; ++j) s[j] = 0.f;
+    // a row that nobody sees is never read: its weight is 0, its V counts as 0
+    const raw* vp = static_cast<const raw*>(a.v_cache) + base + lane * DV;
+    float vf[VB][DV];
+    auto fetch_v = [&](int t0) {
+#pragma unroll
+      for (int t = 0; t < VB; ++t) {
+#pragma unroll
+        for (int e = 0; e < DV; ++e) vf[t][e] = 0.f;
+        if (span.sees(pos + t0 + t)) LoadF32<KV, DV>::run(vp + static_cast<size_t>(t0 + t) * D, vf[t]);
+      }
+    };
     const raw* kp = static_cast<const raw*>(a.k_cache) + base + static_cast<size_t>(tok) * D + part * DQ;
-#pragma unroll (GM > 4 ? 1 : 4)
-    for (int d0 = 0; d0 < DQ; d0 += KCH) {
-      float kf[KCH];
-      LoadF32<KV, KCH>::run(kp + d0, kf);
+#pragma unroll 1
+    for (int d0 = 0; d0 < DQ; d0 += KB) {
+      float kf[KB];
+#pragma unroll
+      for (int i = 0; i < KB; i += 8) LoadF32<KV, 8>::run(kp + d0 + i, kf + i);
+      if (d0 + KB == DQ) fetch_v(0);   // on their way beside the last of K
 #pragma unroll
       for (int j = 0; j < GM; ++j)
 #pragma unroll
-        for (int e = 0; e < KCH; ++e) s[j] = fmaf(q_s[j][part * DQ + d0 + e], kf[e], s[j]);
+        for (int e = 0; e < KB; ++e) s[j] = fmaf(q_s[j][part * DQ + d0 + e], kf[e], s[j]);
     }
     const bool seen = span.sees(pos + tok);
     float corr[GM];
@@ -104,18 +122,17 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
 #pragma unroll
       for (int e = 0; e < DV; ++e) acc[j][e] *= corr[j];
     __syncwarp();
-    const raw* vp = static_cast<const raw*>(a.v_cache) + base + lane * DV;
-#pragma unroll 4
-    for (int t = 0; t < kChunk; ++t) {
-      if (!span.sees(pos + t)) continue;   // what an unseen row holds is never read
-      float vf[DV];
-      LoadF32<KV, DV>::run(vp + static_cast<size_t>(t) * D, vf);
 #pragma unroll
-      for (int j = 0; j < GM; ++j) {
-        const float pj = p_s[warp][t][j];
+    for (int t0 = 0; t0 < kChunk; t0 += VB) {
+      if (t0 > 0) fetch_v(t0);
 #pragma unroll
-        for (int e = 0; e < DV; ++e) acc[j][e] = fmaf(pj, vf[e], acc[j][e]);
-      }
+      for (int t = 0; t < VB; ++t)
+#pragma unroll
+        for (int j = 0; j < GM; ++j) {
+          const float pj = p_s[warp][t0 + t][j];
+#pragma unroll
+          for (int e = 0; e < DV; ++e) acc[j][e] = fmaf(pj, vf[t][e], acc[j][e]);
+        }
     }
     __syncwarp();
   }

@@ -199,6 +199,10 @@ pkv_status decode_window_impl(void* out, const void* q, int32_t q_dtype, const v
   // unit sooner than one of four left alone (512 units of 1,028 tokens: 49 us,
   // 56 with three CTAs of four)
   else if (plan.alike && units > 3 * static_cast<int64_t>(sm_count())) a.ctas_per_sm = 2;
+  // the CUDA-core form has eight warps for up to two CTAs, else four: eight pay
+  // from about 28 chunks on (fp32, 295 units of 416 tokens: 24.5 us with four,
+  // 27.4 with eight; 64 of 464: 12.0 and 11.0; 128 of 624: 28.4 and 19.6)
+  if (!tc && unit_tokens < 448) a.ctas_per_sm = 3;
   const bool tensor_scales = fp8 && !block_scales;
   a.qk_scale = softmax_scale * (tensor_scales ? k_scale : 1.0f) * 1.4426950408889634f;
   a.v_scale = tensor_scales ? v_scale : 1.0f;

@@ -1,17 +1,23 @@
 // CUDA-core form of windowed and block-scaled decode attention: fp32 caches,
-// and any other when the CUDA-core kernels are asked for.  The same chunks, splits and merge as attention_window.cuh; a
-// warp takes every fourth chunk of its split, two lanes share a token in the
-// q.k phase (head_dim / 2 elements each) and the lanes split head_dim for
-// p.V.  All G heads (padded to GM) go together, so a K/V element is read once
-// per CTA.  The block's V scale multiplies p in fp32.
+// and any other when the CUDA-core kernels are asked for.  The same chunks,
+// splits and merge as attention_window.cuh; the W warps of a CTA take the
+// chunks of its split in turn, two lanes share a token in the q.k phase
+// (head_dim / 2 elements each) and the lanes split head_dim for p.V.  All G
+// heads (padded to GM) go together, so a K/V element is read once per CTA.  The
+// block's V scale multiplies p in fp32.  Everything is fp32.
+//
+// Bound by a warp's latency per chunk (copies, then GM sums over 16 lanes), so a
+// chunk's K and V and the next one's block id are in flight together.  Measured
+// (GB300): 4 contexts of up to 128, window 33, 4 / 4 heads, fp32: 3.7 us; 295
+// contexts of 136 to 409, 7 / 1 heads: 24.5 us; 16 of 611, 56 / 8 heads: 19.6 us.
 #pragma once
 
 #include "attention_window.cuh"
 
 namespace pkv {
 
-template <typename KV, typename Q, int D, int GM>
-__global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const WindowArgs a) {
+template <typename KV, typename Q, int D, int GM, int W>
+__global__ void __launch_bounds__(32 * W) decode_window_simt_kernel(const WindowArgs a) {
   using namespace tc;
   constexpr int DQ = D / 2, DV = D / 32;
   constexpr int KB = 32;        // K elements a lane has in flight
@@ -34,11 +40,11 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
   const int c1 = static_cast<int>((split + 1) * n_all / nsplit);
 
   __shared__ float q_s[GM][D];
-  __shared__ float p_s[kWarps][kChunk][GM];
-  __shared__ __align__(16) float merge_s[2 * kWarps * 16 + kWarps * 16 * D];
+  __shared__ float p_s[W][kChunk][GM];
+  extern __shared__ __align__(16) float merge_s[];   // [2][W][16], [W][16][D]
   __shared__ int s_bad, s_last;
   if (threadIdx.x == 0) s_bad = bad_ctx ? kBadLength : 0;
-  for (int i = threadIdx.x; i < GM * D; i += kThreads) {
+  for (int i = threadIdx.x; i < GM * D; i += 32 * W) {
     const int j = i / D, d = i % D;
     q_s[j][d] = j < G ? load_elem<Q>(a.q, (static_cast<size_t>(seq) * a.num_q_heads + kvh * G + j) * D + d) * hs.qk
                       : 0.f;
@@ -57,10 +63,10 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
   const int32_t* trow = a.tables + static_cast<size_t>(seq) * a.max_blocks;
   bool bad = false;
   int next = c0 + warp < c1 ? trow[span.chunk(c0 + warp) * kChunk / T] : 0;
-  for (int c = c0 + warp; c < c1; c += kWarps) {
+  for (int c = c0 + warp; c < c1; c += W) {
     const int pos = span.chunk(c) * kChunk;
     const int blk = next;
-    if (c + kWarps < c1) next = trow[span.chunk(c + kWarps) * kChunk / T];
+    if (c + W < c1) next = trow[span.chunk(c + W) * kChunk / T];
     if (blk < 0 || blk >= a.num_blocks) {   // the same for the whole warp
       bad = true;
       break;
@@ -138,8 +144,8 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
   }
   if (bad && lane == 0) atomicOr(&s_bad, kBadTable);
   float* mS = merge_s;
-  float* lS = mS + kWarps * 16;
-  float* oS = lS + kWarps * 16;
+  float* lS = mS + W * 16;
+  float* oS = lS + W * 16;
 #pragma unroll
   for (int j = 0; j < GM; ++j) {
     if (lane == 0) {
@@ -150,18 +156,41 @@ __global__ void __launch_bounds__(tc::kThreads) decode_window_simt_kernel(const 
     for (int e = 0; e < DV; ++e) oS[(warp * 16 + j) * D + lane * DV + e] = acc[j][e];
   }
   __syncthreads();
-  finish_unit<Q, D, kWarps>(a, mS, lS, oS, kvh, seq, split, nsplit, s_bad, hs.v, merge_s,
-                    static_cast<int>(sizeof(merge_s) / sizeof(float)), &s_last);
+  finish_unit<Q, D, W>(a, mS, lS, oS, kvh, seq, split, nsplit, s_bad, hs.v, merge_s, W * 16 * (D + 2), &s_last);
+}
+
+template <typename KV, typename Q, int D, int GM, int W>
+cudaError_t launch_window_simt_w(const WindowArgs& a, cudaStream_t st) {
+  constexpr int smem = W * 16 * (D + 2) * 4;
+  auto kernel = decode_window_simt_kernel<KV, Q, D, GM, W>;
+  if constexpr (smem > 32 * 1024) {   // more than the default with the static part: opted in, per device
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+    if (!bit || !(configured.load() & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      configured.fetch_or(bit);
+    }
+  }
+  return tc::launch_dependent(kernel, dim3(a.num_kv_heads, a.num_seqs, a.max_splits), 32 * W, smem, st, a);
+}
+
+// Eight warps where at most two CTAs share an SM: a warp's chunk is latency.
+template <typename KV, typename Q, int D, int GM>
+cudaError_t launch_window_simt_g(const WindowArgs& a, cudaStream_t st) {
+  return a.ctas_per_sm <= 2 ? launch_window_simt_w<KV, Q, D, GM, 8>(a, st) : launch_window_simt_w<KV, Q, D, GM, 4>(a, st);
 }
 
 template <typename KV, typename Q, int D>
 pkv_status launch_window_simt_d(const WindowArgs& a, cudaStream_t st) {
-  const dim3 grid(a.num_kv_heads, a.num_seqs, a.max_splits);
   cudaError_t e;
-  if (a.group <= 1) e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 1>, grid, tc::kThreads, 0, st, a);
-  else if (a.group <= 4) e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 4>, grid, tc::kThreads, 0, st, a);
-  else if (a.group <= 8) e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 8>, grid, tc::kThreads, 0, st, a);
-  else e = tc::launch_dependent(decode_window_simt_kernel<KV, Q, D, 16>, grid, tc::kThreads, 0, st, a);
+  if (a.group <= 1) e = launch_window_simt_g<KV, Q, D, 1>(a, st);
+  else if (a.group <= 4) e = launch_window_simt_g<KV, Q, D, 4>(a, st);
+  else if (a.group <= 8) e = launch_window_simt_g<KV, Q, D, 8>(a, st);
+  else e = launch_window_simt_g<KV, Q, D, 16>(a, st);
   if (e != cudaSuccess) return cuda_fail("windowed decode: launch", e);
   return check_launch("windowed decode (CUDA cores)");
 }

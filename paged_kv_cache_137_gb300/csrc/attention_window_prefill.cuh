@@ -28,9 +28,9 @@
 // the boxes of a step go out a lane each.
 //
 // Measured (GB300, 152 SMs), of 1870 TFLOP/s that a library product reaches:
-//   one prompt of 8,192, 32 query / 8 KV heads, window 2,048, bf16:  190 us, 1265 TFLOP/s
-//   16 chunks of 512, 28 / 4 heads, window 1,024, bf16:               86 us, 1020 TFLOP/s
-//   16 block-scaled E4M3 chunks of 512 over 1,024 to 4,096 tokens:   239 us,  920 TFLOP/s
+//   one prompt of 8,192, 32 query / 8 KV heads, window 2,048, bf16:  189 us, 1273 TFLOP/s
+//   16 chunks of 512, 28 / 4 heads, window 1,024, bf16:               84 us, 1050 TFLOP/s
+//   16 block-scaled E4M3 chunks of 512 over 1,024 to 4,096 tokens:   238 us,  924 TFLOP/s
 // What bounds it: a step of both tiles takes 1,300 to 1,450 cycles.  With N =
 // 64 its Q K^T reads 6 KB of shared memory per MMA of 32 tensor cycles (1,280
 // cycles a step at 128 bytes a cycle, with P V); the 16 TMA boxes of a step
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       mbar_init(smem_u32(&o_done[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&q_full[i]), kRows);
+      mbar_init(smem_u32(&q_full[i]), kFp8 ? kRows : 2 * kRows);   // helper threads (and their copies)
       mbar_init(smem_u32(&q_free[i]), 1);
       mbar_init(smem_u32(&o_free[i]), kRows);
       mbar_init(smem_u32(&l_full[i]), kRows);
@@ -678,7 +678,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 #pragma unroll
           for (int X = 0; X < 2; ++X) {
             if (t >= nt[X]) continue;
-            if (t == 0) wait(&q_full[X], units[X] & 1);
+            if (t == 0) {
+              wait(&q_full[X], units[X] & 1);
+              fence_proxy_async();   // copies by threads, before the tensor core reads them
+            }
             // the buffer's step before: its P has been read by P V
             if (buf[X].used) wait(&o_done[2 * X + buf[X].slot], buf[X].par ^ 1);
             tc_fence_after();
@@ -781,6 +784,14 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       }
     };
     auto announce_q = [&](int X) {
+      if constexpr (!kFp8) {
+        // the copies announce themselves, so that this unit's output need not
+        // wait for the next one's queries; who waits for them fences
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&q_full[X])) : "memory");
+        mbar_arrive(smem_u32(&q_full[X]));
+        return;
+      }
+      cp_async_wait();
       if constexpr (kFp8 && kOutBf) {   // the MMA is f16: the thread's own pieces
         uint8_t* qx = q_s + X * S_::kQTile + (qc >> 3) * kQSlab;
 #pragma unroll 4
@@ -807,7 +818,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         // the tile's last S of the unit before is done
         if (loads[X] > 0 && !wait(&q_free[X], (loads[X] - 1) & 1)) return false;
         load_q(u, X);
-        cp_async_wait();
         announce_q(X);
         ++loads[X];
       }
@@ -966,7 +976,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       release_work(k);
       u = v;
     }
-    if (!ok) give_up();
+    if (!ok) {
+      cp_async_wait();
+      give_up();
+    }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
     // every branch around a warp-wide TMEM access is taken by the whole warp
